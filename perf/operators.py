@@ -341,7 +341,7 @@ def _plain_write(store, scale, rows, slots):
     top = x.new_zeros(touched.numel(), heads).index_reduce(0, which, x.abs().amax(2), "amax")
     first = torch.full_like(touched, PAGE).index_reduce(0, which, at, "amin")
     before = torch.where(first[:, None] == 0, 0.0, scale[touched])
-    top = torch.where(top < 2.0 ** -96, 0.0, top)
+    top = torch.where(top < 2.0 ** -64, 0.0, top)
     if store.dtype == torch.int8:
         now = torch.maximum(before, top / 127.0)
     else:
