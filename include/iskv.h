@@ -360,6 +360,171 @@ typedef struct {
 ISKV_API int iskv_decode_attention_noalloc(const iskv_decode_operands* ops, const void* q,
                                            float* out, void* stream);
 
+/* ---- paged 8-bit cache of exact tokens ----------------------------------
+ * The uncompressed-rank counterpart of the low-rank cache above: every token
+ * of every request is kept, its K and V rows as 8-bit codes, in pages of 64
+ * tokens that requests of different lengths take from one pool.  The method's
+ * pages have no counterpart; it serves the layers and requests that the
+ * low-rank factors do not serve well, and is the 8-bit baseline to weigh them
+ * against.  Lengths, block tables and slot maps live on the device, so a
+ * serving step (iskv_page_plan, then per layer iskv_q8_append and
+ * iskv_q8_attention) needs no host synchronization and can be captured in a
+ * CUDA graph and replayed with other lengths.
+ *
+ * All pointers are device memory of the current device (or managed memory),
+ * owned by the caller and borrowed for the stream-ordered duration of the
+ * call; other memory is refused with INVALID_ARG.  The calls allocate
+ * nothing, keep nothing between calls, and enqueue on `stream` without
+ * waiting.  Calls that write the same buffers must be ordered by the caller;
+ * calls on different buffers may overlap.
+ *
+ * Integer arrays are int32.  For request b: lens[b] tokens are stored, token
+ * t of it in row t % 64 of page table[b * width + t / 64].                   */
+#define ISKV_PAGE 64
+
+/* One step of the page tables.  Request b, holding lens[b] tokens, is to
+ * receive add[b] >= 0 more, or has ended (add[b] = -1).  First the pages of
+ * ended requests go back to the stack of free pages (requests in order, each
+ * request's pages in token order: free_pages[n_free ...]); then the new blocks
+ * of the other requests take pages from its top (requests in order, blocks in
+ * order).  Written: the new entries of `table`; free_pages; *n_free_out;
+ * lens_out[b] = lens[b] + add[b] (0 for an ended request); cu[0..batch], the
+ * exclusive sums of the added tokens with their total last; slots[i] = 64 *
+ * page + row of the i-th added token, -1 from cu[batch] on; *status.
+ * Entries of `table` of ended requests are left as they were.
+ * `lens_out` may be `lens` and `n_free_out` may be `n_free`; no other buffers
+ * may overlap.
+ * *status is ISKV_OK, or the step is refused as a whole -- lens_out = lens,
+ * n_free_out = n_free, cu = 0, slots = -1, table and free_pages untouched --
+ * with ISKV_ERR_INVALID_ARG (lens[b] outside 0..64*width, add[b] < -1, n_free
+ * outside 0..pages, or more pages given back than the stack holds) or
+ * ISKV_ERR_CAPACITY (a request longer than 64*width, more added tokens than
+ * `tokens`, or more new pages than are free).
+ * Page numbers are the caller's and are not checked beyond 0..pages-1: where
+ * one lies outside, its tokens get slot -1.
+ * Limits: 0 <= batch <= 8192, width >= 1, pages * 64 < 2^31.
+ * Errors: INVALID_ARG (pointers, sizes), UNSUPPORTED (batch), CUDA.         */
+typedef struct {
+    int32_t batch;              /* requests                                  */
+    int32_t width;              /* columns of table                          */
+    int32_t pages;              /* pages of the pool, entries of free_pages  */
+    int32_t tokens;             /* entries of slots                          */
+    const int32_t* lens;        /* [batch] tokens held                       */
+    const int32_t* add;         /* [batch] tokens to come, -1: ended         */
+    int32_t* table;             /* [batch][width] page numbers               */
+    int32_t* free_pages;        /* [pages] stack of free pages               */
+    const int32_t* n_free;      /* [1] entries of the stack in use           */
+    int32_t* lens_out;          /* [batch]                                   */
+    int32_t* cu;                /* [batch + 1]                               */
+    int32_t* slots;             /* [tokens]                                  */
+    int32_t* n_free_out;        /* [1]                                       */
+    int32_t* status;            /* [1]                                       */
+} iskv_page_plan_args;
+
+ISKV_API int iskv_page_plan(const iskv_page_plan_args* args, void* stream);
+
+/* The pages of one layer.  A row's stored value is code * scale with one
+ * fp32 scale per (page, KV head), for K and for V apart.
+ *   ISKV_CODE_INT8: codes -127..127; scale = the block's largest |x| times
+ *     the fp32 value of 1/127, code = x / scale (fp32 division) rounded half
+ *     to even, at most 127 in magnitude.
+ *   ISKV_CODE_E4M3: codes are e4m3 values; scale = the smallest power of two
+ *     2^e with the block's largest |x| <= 448 * 2^e, code = x / 2^e rounded
+ *     half to even.
+ * A block whose largest value is below 2^-64 is stored as zeros, scale 0.
+ * Scales are 0 or in [2^-72, 2^122]; e4m3 codes are not NaN (iskv_q8_append
+ * writes nothing else).                                                     */
+#define ISKV_CODE_INT8 0
+#define ISKV_CODE_E4M3 1
+
+typedef struct {
+    int32_t pages;              /* pages of the pool; pages * 64 < 2^31      */
+    int32_t kv_heads;           /* KV heads of the layer                     */
+    int32_t head_dim;           /* 128                                       */
+    int32_t page;               /* tokens per page: 64                       */
+    int32_t code;               /* ISKV_CODE_INT8 or ISKV_CODE_E4M3          */
+    void* k;                    /* [pages][kv_heads][64][128] codes          */
+    void* v;
+    float* k_scale;             /* [pages][kv_heads]                         */
+    float* v_scale;
+} iskv_q8_pages;
+
+/* Store n rows of K and V: row i of k ([n][kv_heads][128], elements of
+ * `dtype`, k_stride elements from token to token) goes to slot slots[i]
+ * (64 * page + row), likewise v.  Rows with slot -1 are skipped.  The rows of
+ * one page come as one run of ascending slots within the call (as
+ * iskv_page_plan gives them), and a page belongs to one request.
+ * A run that starts at row 0 begins its page: the page's scale is that of the
+ * run.  A run that starts later extends it: where the new rows need a larger
+ * scale, the page's rows before the run are coded again, from their codes, in
+ * the larger scale (rounded half to even: code * (old scale / new scale)).
+ * Rows of the page behind the run are left as they were.
+ * Elements that are not finite are stored as zeros and set *status to
+ * ISKV_ERR_RANGE; slots outside -1 .. 64*pages-1 are skipped and set it to
+ * ISKV_ERR_INVALID_ARG (the smaller code stays; *status is otherwise left;
+ * NULL: not reported).  k and v must be 16-byte aligned, strides multiples of
+ * 16 bytes.  Errors: INVALID_ARG, UNSUPPORTED (head_dim, page), CUDA.        */
+ISKV_API int iskv_q8_append(const iskv_q8_pages* store, const void* k, const void* v, int dtype,
+                            int64_t k_stride, int64_t v_stride, int64_t n, const int32_t* slots,
+                            int32_t* status, void* stream);
+
+/* Attention of ragged queries over the pages.  Request b's queries are tokens
+ * cu[b] .. cu[b+1]-1 of q ([tokens][q_heads][128], q_stride elements from
+ * token to token) and are the last ones it stores: the last query sits at
+ * position lens[b] - 1, the one before it at lens[b] - 2, and so on (lens as
+ * iskv_page_plan leaves them in lens_out, after iskv_q8_append).  Query head
+ * j reads KV head j / (q_heads / kv_heads).  A query at position p scores the
+ * key at position t < lens[b]
+ *     x = scale * q . k            (keys as appended: rotate them before)
+ *     x = cap * tanh(x / cap)      where cap > 0
+ *     x = x - slopes[j] * |p - t|  where slopes is not NULL
+ * and sees it where
+ *     (t <= p and (window = 0 or t > p - window)) or t < prefix[b]
+ * (prefix NULL: 0): causal, with a sliding window where window > 0, and a
+ * prefix that every query of the request sees whole.  One softmax over what
+ * it sees; out ([tokens][q_heads][128], contiguous, in dtype) is the weighted
+ * sum of V, zeros where a query sees nothing (lens[b] smaller than the number
+ * of its queries).  Rows of out from cu[batch] on are left as they were.
+ * `max_new` tells the host the largest number of queries of one request (it
+ * picks the kernel; a wrong value costs time, not results).  A page number
+ * outside 0..pages-1 hides its tokens; lens is taken as at most 64 * width.
+ * The workspace (iskv_q8_workspace bytes, 16-byte aligned, any contents)
+ * belongs to the call until the stream has passed it: calls that may overlap
+ * need one each.
+ * q_heads / kv_heads <= 8; ISKV_BF16 or ISKV_F32 queries; q, out and
+ * workspace 16-byte aligned, q_stride a multiple of 16 bytes.
+ * Errors: INVALID_ARG, UNSUPPORTED (head_dim, page, heads per group),
+ * CAPACITY (workspace too small), CUDA.                                     */
+typedef struct {
+    int32_t batch;              /* requests, 0 .. 8192                       */
+    int32_t width;              /* columns of table                          */
+    int32_t q_heads;
+    int32_t dtype;              /* of q and out                              */
+    int32_t max_new;
+    int32_t window;             /* 0: none                                   */
+    float scale;                /* > 0; usually 1 / sqrt(128)                */
+    float cap;                  /* 0: none                                   */
+    int64_t tokens;             /* rows of q and out                         */
+    int64_t q_stride;           /* elements                                  */
+    const void* q;
+    void* out;
+    const int32_t* table;       /* [batch][width]                            */
+    const int32_t* lens;        /* [batch]                                   */
+    const int32_t* cu;          /* [batch + 1]                               */
+    const int32_t* prefix;      /* [batch], or NULL                          */
+    const float* slopes;        /* [q_heads], or NULL                        */
+    void* workspace;
+    int64_t workspace_bytes;
+} iskv_q8_attention_args;
+
+ISKV_API int iskv_q8_attention(const iskv_q8_pages* store, const iskv_q8_attention_args* args,
+                               void* stream);
+
+/* Workspace bytes of an iskv_q8_attention call on the current device with
+ * these sizes (host only); -1 for sizes that it refuses.                    */
+ISKV_API int64_t iskv_q8_workspace(int32_t q_heads, int32_t kv_heads, int64_t tokens, int32_t max_new,
+                                   int32_t dtype);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,7 +18,7 @@ import torch
 
 __all__ = ["Config", "Cache", "IskvError", "DecodeOperands", "QuantFormat", "quantize_rows",
            "lib_path", "LIB", "F32", "BF16", "WHICH_K", "WHICH_V", "ALL_LAYERS", "FOLD_DEFER_SYNC",
-           "EXPORTED"]
+           "EXPORTED", "PAGE", "CODE_INT8", "CODE_E4M3", "PagePlan", "page_plan", "Q8Pages"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 
@@ -39,6 +39,8 @@ F32, BF16 = 0, 1
 WHICH_K, WHICH_V = 0, 1
 ALL_LAYERS = -1
 FOLD_DEFER_SYNC = 1
+PAGE = 64
+CODE_INT8, CODE_E4M3 = 0, 1
 
 _ERRORS = {-1: "INVALID_ARG", -2: "CAPACITY", -3: "STATE", -4: "CUDA", -5: "NOCONVERGE",
            -6: "NOMEM", -7: "UNSUPPORTED", -8: "DEVICE_TIMEOUT", -9: "RANGE"}
@@ -87,6 +89,28 @@ class DecodeOperands(ctypes.Structure):
                                        "ring_v", "rope")]
 
 
+class _PlanArgs(ctypes.Structure):
+    """Mirror of ``iskv_page_plan_args``."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "width", "pages", "tokens")] + [
+        (n, ctypes.c_void_p) for n in ("lens", "add", "table", "free_pages", "n_free", "lens_out", "cu",
+                                       "slots", "n_free_out", "status")]
+
+
+class _Q8Pages(ctypes.Structure):
+    """Mirror of ``iskv_q8_pages``."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("pages", "kv_heads", "head_dim", "page", "code")] + [
+        (n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
+
+
+class _Q8Attention(ctypes.Structure):
+    """Mirror of ``iskv_q8_attention_args``."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "width", "q_heads", "dtype", "max_new", "window")] + [
+        (n, ctypes.c_float) for n in ("scale", "cap")] + [
+        (n, ctypes.c_int64) for n in ("tokens", "q_stride")] + [
+        (n, ctypes.c_void_p) for n in ("q", "out", "table", "lens", "cu", "prefix", "slopes", "workspace")] + [
+        ("workspace_bytes", ctypes.c_int64)]
+
+
 _vp, _i, _i64p = ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(ctypes.c_int64)
 _SIGS = {
     "iskv_config_default": ([ctypes.POINTER(_Cfg)], _i),
@@ -107,6 +131,12 @@ _SIGS = {
     "iskv_decode_attention_noalloc": ([ctypes.POINTER(DecodeOperands), _vp, _vp, _vp], _i),
     "iskv_quantize_rows": ([ctypes.POINTER(QuantFormat), _i, _vp, ctypes.c_int64, _vp, _vp, _vp], _i),
     "iskv_quant_words": ([ctypes.POINTER(QuantFormat)], _i),
+    "iskv_page_plan": ([ctypes.POINTER(_PlanArgs), _vp], _i),
+    "iskv_q8_append": ([ctypes.POINTER(_Q8Pages), _vp, _vp, _i, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                        _vp, _vp, _vp], _i),
+    "iskv_q8_attention": ([ctypes.POINTER(_Q8Pages), ctypes.POINTER(_Q8Attention), _vp], _i),
+    "iskv_q8_workspace": ([ctypes.c_int32, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32],
+                          ctypes.c_int64),
 }
 for _name, (_args, _ret) in _SIGS.items():
     _fn = getattr(LIB, _name)
@@ -319,3 +349,186 @@ def quantize_rows(groups, rows: torch.Tensor, stream=None):
     _check(LIB.iskv_quantize_rows(ctypes.byref(fmt), rank, _ptr(rows), n, _ptr(codes), _ptr(scales),
                                   _stream(stream)), "iskv_quantize_rows")
     return codes, scales
+
+
+# ---------------------------------------------------------------------------
+# Paged 8-bit cache of exact tokens
+# ---------------------------------------------------------------------------
+_CODE_DT = {CODE_INT8: torch.int8, CODE_E4M3: torch.float8_e4m3fn}
+_DT_CODE = {d: c for c, d in _CODE_DT.items()}
+_DT_ELEM = {d: e for e, d in _TORCH_DT.items()}
+
+
+def _launch(device: torch.device, fn, where: str, *args, stream=None) -> None:
+    """Call a library function that takes the stream last, on `device`."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _launch(device, fn, where, *args, stream=stream)
+    code = fn(*args, _stream(stream))
+    if code != OK:
+        raise IskvError(code, where)
+
+
+def _int32(device, shape, t, name):
+    if t.dtype != torch.int32 or t.device != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _on_cuda(t: torch.Tensor, name: str) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    return t.device
+
+
+@dataclass
+class PagePlan:
+    """What one step of the page tables gives (int32, on the device): the
+    lengths after the step [batch], cu [batch + 1] (exclusive sums of the added
+    tokens), slots [tokens], n_free [1], status [1]."""
+    lens: torch.Tensor
+    cu: torch.Tensor
+    slots: torch.Tensor
+    n_free: torch.Tensor
+    status: torch.Tensor
+
+    @classmethod
+    def empty(cls, batch: int, tokens: int, device="cuda") -> "PagePlan":
+        def e(n):
+            return torch.empty(n, dtype=torch.int32, device=device)
+        return cls(e(batch), e(batch + 1), e(tokens), e(1), e(1))
+
+
+def page_plan(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, free: torch.Tensor,
+              n_free: torch.Tensor, tokens: int | None = None, out: PagePlan | None = None,
+              stream=None) -> PagePlan:
+    """One step of the page tables on the GPU (``iskv_page_plan``): request b
+    holds lens[b] tokens and gets add[b] more, or has ended (-1).  `table`
+    [batch, width] and the stack `free` [pages], of which `n_free` [1] entries
+    are in use, are updated in place; the new lengths, slots and stack size go
+    to `out` (or to new tensors for `tokens` slots).  To step in place, pass an
+    `out` whose lens and n_free are the inputs.  ``status`` is 0, or the
+    negative error code of a step that was refused as a whole."""
+    dev = _on_cuda(lens, "lens")
+    if lens.dim() != 1 or table.dim() != 2 or free.dim() != 1:
+        raise ValueError("lens and free must be 1-d, table 2-d")
+    batch, width = lens.shape[0], table.shape[1]
+    if out is None:
+        if tokens is None:
+            raise ValueError("tokens (the number of slots) or out is needed")
+        out = PagePlan.empty(batch, tokens, dev)
+    n = out.slots.shape[0]
+    one = (1,)
+    args = _PlanArgs(batch, width, free.shape[0], n, _int32(dev, (batch,), lens, "lens"),
+                     _int32(dev, (batch,), add, "add"), _int32(dev, (batch, width), table, "table"),
+                     _int32(dev, free.shape, free, "free"), _int32(dev, one, n_free, "n_free"),
+                     _int32(dev, (batch,), out.lens, "out.lens"), _int32(dev, (batch + 1,), out.cu, "out.cu"),
+                     _int32(dev, (n,), out.slots, "out.slots"), _int32(dev, one, out.n_free, "out.n_free"),
+                     _int32(dev, one, out.status, "out.status"))
+    _launch(dev, LIB.iskv_page_plan, "iskv_page_plan", ctypes.byref(args), stream=stream)
+    return out
+
+
+class Q8Pages:
+    """The pages of one layer: K and V rows as 8-bit codes, 64 tokens a page,
+    one scale per page and KV head.  ``k``, ``v`` [pages, kv_heads, 64, 128]
+    (int8 or float8_e4m3fn) and ``k_scale``, ``v_scale`` [pages, kv_heads] are
+    ordinary tensors; a stored row is codes * scale.  Requests take pages by
+    ``page_plan``.  Forward only."""
+
+    def __init__(self, pages: int, kv_heads: int, code: int = CODE_INT8, device="cuda"):
+        if code not in _CODE_DT:
+            raise ValueError("code must be CODE_INT8 or CODE_E4M3")
+        shape = (pages, kv_heads, PAGE, 128)
+        bits = [torch.zeros(shape, dtype=torch.int8, device=device) for _ in range(2)]
+        scale = [torch.zeros(pages, kv_heads, dtype=torch.float32, device=device) for _ in range(2)]
+        self._take(bits[0].view(_CODE_DT[code]), bits[1].view(_CODE_DT[code]), *scale)
+
+    @classmethod
+    def of(cls, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor) -> "Q8Pages":
+        """Pages in the caller's own tensors."""
+        self = cls.__new__(cls)
+        self._take(k, v, k_scale, v_scale)
+        return self
+
+    def _take(self, k, v, k_scale, v_scale):
+        dev = _on_cuda(k, "k")
+        if k.dtype not in _DT_CODE or v.dtype != k.dtype:
+            raise TypeError("k and v must both be int8 or both float8_e4m3fn")
+        if k.dim() != 4 or tuple(k.shape[2:]) != (PAGE, 128) or v.shape != k.shape:
+            raise ValueError(f"k and v must be [pages, kv_heads, {PAGE}, 128]")
+        for t, shape, dt in ((v, k.shape, k.dtype), (k_scale, k.shape[:2], torch.float32),
+                             (v_scale, k.shape[:2], torch.float32)):
+            if t.shape != shape or t.dtype != dt or t.device != dev:
+                raise ValueError("v, k_scale and v_scale must match k in shape, device and type")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device, self.kv_heads = dev, k.shape[1]
+        self._status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._c = _Q8Pages(k.shape[0], k.shape[1], 128, PAGE, _DT_CODE[k.dtype], _ptr(k), _ptr(v), _ptr(k_scale),
+                           _ptr(v_scale))
+
+    def _rows(self, t: torch.Tensor, heads: int | None, name: str) -> int:
+        if t.dim() != 3 or t.shape[2] != 128 or (heads is not None and t.shape[1] != heads) \
+                or (t.shape[0] > 0 and t.stride()[1:] != (128, 1)):
+            raise ValueError(f"{name} must be [tokens, heads, 128] with contiguous tokens")
+        if t.device != self.device:
+            raise ValueError(f"{name} must be on {self.device}")
+        if t.dtype not in _DT_ELEM:
+            raise TypeError(f"{name} must be bfloat16 or float32")
+        return _DT_ELEM[t.dtype]
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
+        """Store rows k, v [n, kv_heads, 128] (any token stride) in the slots
+        [n] that ``page_plan`` gave; rows with slot -1 are skipped."""
+        dt = self._rows(k, self.kv_heads, "k")
+        if self._rows(v, self.kv_heads, "v") != dt or v.shape != k.shape:
+            raise ValueError("k and v must agree in shape and type")
+        n = k.shape[0]
+        _launch(self.device, LIB.iskv_q8_append, "iskv_q8_append", ctypes.byref(self._c), k.data_ptr(), v.data_ptr(),
+                dt, k.stride(0), v.stride(0), n, _int32(self.device, (n,), slots, "slots"), self._status.data_ptr(),
+                stream=stream)
+
+    def attention(self, q: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, cu: torch.Tensor, max_new: int,
+                  scale: float = 128 ** -0.5, cap: float = 0.0, slopes: torch.Tensor | None = None,
+                  window: int = 0, prefix: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+        """Attention of q [tokens, q_heads, 128] (any token stride): request
+        b's queries are rows cu[b]:cu[b+1] and the last of its lens[b] stored
+        tokens.  Causal; `window` > 0 limits how far back a query sees,
+        prefix[b] tokens at the start are seen by all; `cap` caps scores by
+        cap*tanh(x/cap); slopes[q_heads] (fp32) take slope * distance off.
+        `max_new` is the largest number of queries of one request.  Returns
+        out [tokens, q_heads, 128] in q's type."""
+        dt = self._rows(q, None, "q")
+        n, heads = q.shape[0], q.shape[1]
+        dev = self.device
+        if q.requires_grad and torch.is_grad_enabled():
+            raise ValueError("attention over 8-bit pages is forward only: detach q")
+        if out is None:
+            out = torch.empty(n, heads, 128, dtype=q.dtype, device=dev)
+        elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
+            raise ValueError("out must be contiguous and match q in shape, type and device")
+        if lens.dim() != 1 or table.dim() != 2:
+            raise ValueError("lens must be 1-d, table 2-d")
+        batch, width = lens.shape[0], table.shape[1]
+        if slopes is not None and (slopes.dtype != torch.float32 or tuple(slopes.shape) != (heads,)
+                                   or slopes.device != dev or not slopes.is_contiguous()):
+            raise ValueError("slopes must be a contiguous fp32 tensor [q_heads] on the pages' device")
+        need = LIB.iskv_q8_workspace(heads, self.kv_heads, n, max_new, dt)
+        ws = torch.empty(max(need, 0), dtype=torch.uint8, device=dev)
+        args = _Q8Attention(batch, width, heads, dt, max_new, window, scale, cap, n, q.stride(0), q.data_ptr(),
+                            out.data_ptr(), _int32(dev, (batch, width), table, "table"),
+                            _int32(dev, (batch,), lens, "lens"), _int32(dev, (batch + 1,), cu, "cu"),
+                            None if prefix is None else _int32(dev, (batch,), prefix, "prefix"),
+                            None if slopes is None else slopes.data_ptr(), ws.data_ptr(), need)
+        if stream is not None:   # the workspace comes from the current stream's pool
+            ws.record_stream(stream)
+        _launch(dev, LIB.iskv_q8_attention, "iskv_q8_attention", ctypes.byref(self._c), ctypes.byref(args),
+                stream=stream)
+        return out
+
+    def status(self) -> int:
+        """Synchronize and return the sticky status of the appends: 0, or the
+        code of non-finite rows (RANGE) or slots outside the pool
+        (INVALID_ARG)."""
+        return int(self._status.item())

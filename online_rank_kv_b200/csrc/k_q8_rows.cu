@@ -1,0 +1,703 @@
+// iskv_q8_attention for few query rows per KV head: single tokens, drafts to
+// verify, fp32 queries.  Split along the keys over the whole GPU.
+//
+// Mathematics.  Keys and values are codes times one scale per page and head,
+// so the scale leaves the dot products: with c the codes,
+//     score = (scale s_k) (q . c_k),   out = sum w s_v c_v / sum w.
+// One exponential carries the value scale too: with
+//     w = 2^(score log2 e + log2 s_v - M),  M the running maximum,
+// the numerator is sum w c_v and the denominator sum w / s_v, whose factor
+// 1 / s_v is one number per page.  Codes are exact in fp16.  Queries are
+// multiplied by a power of two per row (their largest element then lies in
+// [2^14, 2^15)) and are exact in fp16 down to 2^-38 of it for bf16 input; fp32
+// queries, and the weights that go with them, take two fp16 parts (22 bits).
+// For bf16 queries the weights are rounded to fp16 (2^-12 relative, an eighth
+// of the output's own rounding); sums and maxima stay in fp32.
+//
+// Layout.  The products are taken transposed: S^T = K Q^T and O^T = V^T P^T,
+// so that the keys fill the 16 rows of m16n8k16 and the few query rows its 8
+// columns (half the instructions of the other order when there are at most 8
+// rows), and a lane ends up with 16 consecutive output elements of its two
+// rows.  P^T turns from accumulator to operand layout by movmatrix.  The order
+// of the 128 elements inside a dot product is free, so a lane takes 32
+// consecutive codes of a key row (two 16-byte loads) instead of the
+// instruction's interleaved pairs.  Tensor cores carry it by mma.sync here: at
+// 8 columns the kernel needs about a tenth of their rate, and waits for memory.
+//
+// Work.  Requests, heads, row tiles and 32-token steps are numbered through;
+// every CTA finds its equal share of the steps from the lengths itself (one
+// pass over the requests, no plan on the host) and every warp its share of
+// that, so lengths may differ freely.  A warp runs its own three-stage
+// cp.async pipeline (4 KB of K and 4 KB of V per stage) and never waits for
+// another warp until its share is done.  What one warp finishes alone is
+// written at once; what several warps share is joined in the CTA, what several
+// CTAs share by a second small kernel.
+#include "q8_common.cuh"
+
+namespace iskv {
+namespace q8 {
+
+namespace {
+
+constexpr int kWarps = kRowWarps;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kStages = 3;
+constexpr int kStoreBytes = kStepTokens * kHeadDim;      // K or V of one step: 4 KB
+constexpr int kStageBytes = 2 * kStoreBytes;
+constexpr int kSmemBytes = kWarps * kStages * kStageBytes;
+
+using Req = Seen<kStepTokens>;
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack(uint32_t x) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&x));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+
+// A place in the numbered-through steps.
+struct Cursor {
+    int b, item, step;    // request, head * tiles + tile, step
+    int tiles;
+    Req r;
+    __device__ __forceinline__ void load(const AttnArgs& p) {
+        r = seen_of<kStepTokens>(p, b);
+        tiles = (r.n + p.tq - 1) / p.tq;
+    }
+    __device__ __forceinline__ void start(const AttnArgs& p, int b_, int64_t off) {
+        b = b_;
+        load(p);
+        item = (int)(off / r.steps);
+        step = (int)(off % r.steps);
+    }
+    // to the next step; the caller knows that there is one
+    __device__ __forceinline__ void next(const AttnArgs& p) {
+        if (++step < r.steps) return;
+        step = 0;
+        if (++item < tiles * p.kv_heads) return;
+        item = 0;
+        do {
+            ++b;
+            load(p);
+        } while (r.steps == 0);
+    }
+};
+
+// What the CTA knows of each of its warps' two partials.
+struct Part {
+    int64_t id;       // request << 32 | item, -1: none
+    int begins, ends; // whether it holds the item's first / last step
+};
+
+__device__ __forceinline__ int64_t units_of(const AttnArgs& p, int b) {
+    const Req r = seen_of<kStepTokens>(p, b);
+    return (int64_t)((r.n + p.tq - 1) / p.tq) * r.steps * p.kv_heads;
+}
+
+// Row n of an item: its query token and head, or false.
+__device__ __forceinline__ bool row_of(const AttnArgs& p, const Req& r, int item, int tiles, int n, int* token, int* head) {
+    const int h = item / tiles, tile = item % tiles;
+    const int k = n / p.g;
+    *token = tile * p.tq + k;
+    *head = h * p.g + n % p.g;
+    return k < p.tq && *token < r.n;
+}
+
+template <bool F32>
+__device__ __forceinline__ void store_out(const AttnArgs& p, int64_t at, const float* v, int n) {
+    // n consecutive elements (a multiple of 4)
+    if (F32) {
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+        for (int i = 0; i < n / 4; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else {
+        uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at);
+        for (int i = 0; i < n / 4; ++i) {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(v[4 * i], v[4 * i + 1]);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[4 * i + 2], v[4 * i + 3]);
+            o[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+        }
+    }
+}
+
+// Joins `n` partials of R rows, read through `at(i)` (the i-th partial's
+// index), into one: either the final rows of `item` or partial `to`.
+template <int R, bool F32, typename At>
+__device__ __forceinline__ void join(const AttnArgs& p, int n, At at, int to, int b, int item) {
+    const Req r = seen_of<kStepTokens>(p, b);
+    const int tiles = (r.n + p.tq - 1) / p.tq;
+    for (int e = threadIdx.x; e < R * 32; e += blockDim.x) {
+        const int row = e >> 5, d = (e & 31) * 4;
+        int token, head;
+        if (!row_of(p, r, item, tiles, row, &token, &head)) continue;
+        float M = -INFINITY;
+        for (int i = 0; i < n; ++i) M = fmaxf(M, p.ml[((int64_t)at(i) * R + row) * 2]);
+        const float base = M == -INFINITY ? 0.f : M;
+        float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const int64_t k = (int64_t)at(i) * R + row;
+            const float2 ml = *reinterpret_cast<const float2*>(p.ml + k * 2);
+            const float4 v = *reinterpret_cast<const float4*>(p.part + k * kHeadDim + d);
+            const float w = ex2(ml.x - base);
+            l += w * ml.y;
+            o[0] += w * v.x;
+            o[1] += w * v.y;
+            o[2] += w * v.z;
+            o[3] += w * v.w;
+        }
+        if (to < 0) {
+            const float inv = l > 0.f ? __fdiv_rn(1.f, l) : (l == 0.f ? 0.f : l);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] *= inv;
+            store_out<F32>(p, ((int64_t)(r.first + token) * p.kv_heads * p.g + head) * kHeadDim + d, o, 4);
+        } else {
+            const int64_t k = (int64_t)to * R + row;
+            *reinterpret_cast<float4*>(p.part + k * kHeadDim + d) = make_float4(o[0], o[1], o[2], o[3]);
+            if (d == 0) *reinterpret_cast<float2*>(p.ml + k * 2) = make_float2(M, l);
+        }
+    }
+}
+
+// Meta words per CTA: [0] whether its partial 0 ends an item; [1] CTAs that
+// follow with the rest of the item that its partial 1 begins (0: none); [2]
+// that item's request, [3] its item.
+constexpr int kMeta = 4;
+
+template <int CODE, int NT, bool F32, bool MOD>
+__global__ void __launch_bounds__(kThreads, 1) q8_rows_kernel(const AttnArgs p) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t s_scan[kWarps], s_off[kWarps];
+    __shared__ int s_b[kWarps];
+    __shared__ Part s_part[kWarps][2];
+    __shared__ int s_page[kWarps][kStages];
+    constexpr int R = 8 * NT, PARTS = F32 ? 2 : 1;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int r = lane >> 2, q = lane & 3;
+    const int cta = blockIdx.x;
+
+    // ---- this CTA's and this warp's share of the steps --------------------
+    const int chunk = (p.batch + kThreads - 1) / kThreads;
+    const int b0 = min(p.batch, t * chunk), b1 = min(p.batch, b0 + chunk);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += units_of(p, b);
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    if (t < kWarps) s_part[t][0].id = s_part[t][1].id = -1;
+    __syncthreads();
+    int64_t total = 0, ex = incl - mine;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) ex += s_scan[w];
+        total += s_scan[w];
+    }
+    const int64_t per_cta = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t u0 = cta * per_cta, u1 = min(total, u0 + per_cta);
+    if (u0 >= u1) {   // uniform over the CTA
+        if (t < kMeta) p.meta[cta * kMeta + t] = 0;
+        return;
+    }
+    const int64_t per_warp = (u1 - u0 + kWarps - 1) / kWarps;
+    if (mine > 0) {
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const int64_t u = u0 + w * per_warp;
+            if (u < u1 && u >= ex && u < ex + mine) {
+                int64_t off = u - ex;
+                int b = b0;
+                for (;; ++b) {
+                    const int64_t n = units_of(p, b);
+                    if (off < n) break;
+                    off -= n;
+                }
+                s_b[w] = b;
+                s_off[w] = off;
+            }
+        }
+    }
+    __syncthreads();
+
+    const int64_t w0 = u0 + warp * per_warp;
+    const int64_t left = min(u1, w0 + per_warp) - w0;   // steps of this warp (may be <= 0)
+    uint8_t* ring = smem + warp * (kStages * kStageBytes);
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+    const int my_parts = (cta * kPartsPerCta) + 2 * warp;
+
+    if (left > 0) {
+        Cursor in, at;
+        in.start(p, s_b[warp], s_off[warp]);
+        at = in;
+
+        // ---- loads: step i of this warp into stage i % kStages ------------
+        auto page_of = [&](const Cursor& c) {
+            const int tok = c.r.step_of(c.step) * kStepTokens;
+            return tok < c.r.len ? p.table[(int64_t)c.b * p.width + tok / kPage] : -1;
+        };
+        auto issue = [&](const Cursor& c, int page, int stage) {
+            const int tok = c.r.step_of(c.step) * kStepTokens;
+            const int h = c.item / c.tiles;
+            const bool ok = page >= 0 && page < p.pages;
+            const int rows = ok ? c.r.len - tok : 0;   // rows of the step that are stored
+            const int64_t base = ((int64_t)(ok ? page : 0) * p.kv_heads + h) * (kPage * kHeadDim) +
+                                 (tok % kPage) * kHeadDim;
+            const int ch = lane & 7, row = lane >> 3;
+            const uint32_t dst = ring_at + stage * kStageBytes;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int rr = row + 4 * i;
+                const uint32_t d = dst + rr * kHeadDim + ((ch ^ (rr & 7)) << 4);
+                const int64_t s = base + rr * kHeadDim + ch * 16;
+                const uint32_t bytes = rr < rows ? 16u : 0u;   // rows behind the end read as zeros
+                cp16(d, p.k + s, bytes);
+                cp16(d + kStoreBytes, p.v + s, bytes);
+            }
+            if (lane == 0) s_page[warp][stage] = ok ? page : -1;
+        };
+        int64_t issued = 0;
+        int page = page_of(in);
+#pragma unroll
+        for (int s = 0; s < kStages - 1; ++s) {
+            if (issued < left) {
+                issue(in, page, s);
+                if (++issued < left) {
+                    in.next(p);
+                    page = page_of(in);
+                }
+            }
+            cp_commit();
+        }
+
+        uint32_t qf[PARTS][NT][8][2];          // queries as B fragments
+        float rowf[NT][2];                     // score factor of rows 2q, 2q + 1 of each tile of 8
+        int pos[NT][2], seen_to[NT][2], seen_from[NT][2];   // the causal span (seen_from, seen_to]
+        float slope[NT][2];
+        float M[NT][2], l[NT][2], o[NT][8][4];
+        int pmin = 0, pmax = 0;
+
+        auto begin = [&]() {   // of an item: its queries
+            int token, head;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float x[32];
+                const bool on = row_of(p, at.r, at.item, at.tiles, n * 8 + r, &token, &head);
+                const int64_t src = (int64_t)(at.r.first + token) * p.q_stride + head * kHeadDim + 32 * q;
+                if (F32) {
+                    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + src);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 v = on ? __ldg(s + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+                    }
+                } else {
+                    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + src);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 v = on ? __ldg(s + i) : make_uint4(0u, 0u, 0u, 0u);
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            x[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
+                            x[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+                        }
+                    }
+                }
+                float top = 0.f;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(x[i]));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // 2^up brings the row's largest element into [2^14, 2^15)
+                int up = 14 - ((int)(__float_as_uint(top) >> 23) - 127);
+                up = max(-126, min(126, up));
+                const float f = __uint_as_float((uint32_t)(up + 127) << 23);
+                const float down = __uint_as_float((uint32_t)(127 - up) << 23) * (p.scale * (MOD ? 1.f : kLog2e));
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float a = x[4 * s + 2 * i] * f, b = x[4 * s + 2 * i + 1] * f;
+                        qf[0][n][s][i] = pack(a, b);
+                        if (F32) {
+                            const float2 hi = unpack(qf[0][n][s][i]);
+                            qf[PARTS - 1][n][s][i] = pack(a - hi.x, b - hi.y);
+                        }
+                    }
+                }
+                rowf[n][0] = __shfl_sync(0xffffffffu, down, 8 * q);
+                rowf[n][1] = __shfl_sync(0xffffffffu, down, 8 * q + 4);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const bool there = row_of(p, at.r, at.item, at.tiles, n * 8 + 2 * q + i, &token, &head);
+                    pos[n][i] = at.r.len - at.r.n + min(token, at.r.n - 1);
+                    slope[n][i] = MOD && p.slopes && there ? p.slopes[head] * kLog2e : 0.f;
+                    seen_to[n][i] = pos[n][i];
+                    seen_from[n][i] = p.window > 0 ? max(-1, pos[n][i] - p.window) : -1;
+                    M[n][i] = -INFINITY;
+                    l[n][i] = 0.f;
+                }
+#pragma unroll
+                for (int m = 0; m < 8; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[n][m][i] = 0.f;
+            }
+            const int tile = at.item % at.tiles;
+            pmin = at.r.len - at.r.n + tile * p.tq;
+            pmax = min(at.r.len - 1, pmin + p.tq - 1);
+        };
+
+        int first_step = at.step;
+        begin();
+        for (int64_t i = 0; i < left; ++i) {
+            // keep kStages - 1 steps in flight
+            if (issued < left) {
+                issue(in, page, (int)(issued % kStages));
+                if (++issued < left) {
+                    in.next(p);
+                    page = page_of(in);
+                }
+            }
+            cp_commit();
+            cp_wait<kStages - 1>();
+            __syncwarp();
+            const int stage = (int)(i % kStages);
+            const int this_page = s_page[warp][stage];
+            const int tok = at.r.step_of(at.step) * kStepTokens;
+            const int stop = this_page < 0 ? 0 : at.r.len;      // stored tokens end here
+            const int h = at.item / at.tiles;
+            const int64_t block = (int64_t)max(this_page, 0) * p.kv_heads + h;
+            const float sk = __ldg(p.k_scale + block);
+            float sv = __ldg(p.v_scale + block);
+            sv = sv > 0.f ? sv : 1.f;                             // a block of zeros
+            const uint32_t kb = ring_at + stage * kStageBytes, vb = kb + kStoreBytes;
+
+            // ---- S^T = K Q^T: two tiles of 16 tokens ----------------------
+            float sc[NT][2][4];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                uint32_t c0[8], c1[8];   // codes 32q .. 32q + 31 of tokens 16m + r and 16m + r + 8
+                const int ra = 16 * m + r;
+                {
+                    const uint32_t ka = kb + ra * kHeadDim, kc = ka + 8 * kHeadDim;
+                    const uint4 a = lds128(ka + (((2 * q) ^ (ra & 7)) << 4)), b = lds128(ka + (((2 * q + 1) ^ (ra & 7)) << 4));
+                    const uint4 c = lds128(kc + (((2 * q) ^ (ra & 7)) << 4)), d = lds128(kc + (((2 * q + 1) ^ (ra & 7)) << 4));
+                    c0[0] = a.x; c0[1] = a.y; c0[2] = a.z; c0[3] = a.w;
+                    c0[4] = b.x; c0[5] = b.y; c0[6] = b.z; c0[7] = b.w;
+                    c1[0] = c.x; c1[1] = c.y; c1[2] = c.z; c1[3] = c.w;
+                    c1[4] = d.x; c1[5] = d.y; c1[6] = d.z; c1[7] = d.w;
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[n][m][e] = 0.f;
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    const uint32_t x0 = Codes<CODE>::bias(c0[s]), x1 = Codes<CODE>::bias(c1[s]);
+                    const uint32_t a[4] = {Codes<CODE>::lo(x0), Codes<CODE>::lo(x1), Codes<CODE>::hi(x0), Codes<CODE>::hi(x1)};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int z = 0; z < PARTS; ++z) mma16816(sc[n][m], a, qf[z][n][s][0], qf[z][n][s][1]);
+                }
+            }
+
+            // ---- weights ---------------------------------------------------
+            const float lsv = lg2(sv), isv = __fdividef(1.f, sv);
+            const bool whole = tok + kStepTokens <= stop &&
+                               ((tok + kStepTokens - 1 <= pmin && (p.window == 0 || tok > pmax - p.window)) ||
+                                tok + kStepTokens <= at.r.pre);
+            uint32_t pf[PARTS][NT][2][2];   // P^T as B fragments: [16-token half][8 tokens]
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int c = e & 1, key = tok + 16 * m + r + 8 * (e >> 1);
+                        float x = sc[n][m][e] * (rowf[n][c] * sk);
+                        if (MOD) {
+                            if (p.cap > 0.f) x = p.cap * tanh_abs(__fdividef(x, p.cap));
+                            x *= kLog2e;
+                            x -= slope[n][c] * fabsf((float)(pos[n][c] - key));
+                        }
+                        x += lsv;
+                        if (!whole) {
+                            const bool on = key < stop && ((key <= seen_to[n][c] && key > seen_from[n][c]) || key < at.r.pre);
+                            x = on ? x : -INFINITY;
+                        }
+                        sc[n][m][e] = x;
+                        top[c] = fmaxf(top[c], x);
+                    }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], 4));
+                    top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], 8));
+                    top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], 16));
+                }
+                const bool grew = top[0] > M[n][0] || top[1] > M[n][1];
+                if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float now = fmaxf(M[n][c], top[c]);
+                        const float f = now == -INFINITY ? 1.f : ex2(M[n][c] - now);
+                        M[n][c] = now;
+                        l[n][c] *= f;
+#pragma unroll
+                        for (int m = 0; m < 8; ++m) {
+                            o[n][m][c] *= f;
+                            o[n][m][c + 2] *= f;
+                        }
+                    }
+                }
+                float sum[2] = {0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float base = (M[n][c] == -INFINITY ? 0.f : M[n][c]) - kWeightShift;
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int e = c; e < 4; e += 2) {
+                            sc[n][m][e] = ex2(sc[n][m][e] - base);
+                            sum[c] += sc[n][m][e];
+                        }
+                    l[n][c] += sum[c] * isv;
+                }
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int i2 = 0; i2 < 2; ++i2) {
+                        const float a = sc[n][m][2 * i2], b = sc[n][m][2 * i2 + 1];
+                        const uint32_t hi = pack(a, b);
+                        pf[0][n][m][i2] = transpose8(hi);
+                        if (F32) {
+                            const float2 f = unpack(hi);
+                            pf[PARTS - 1][n][m][i2] = transpose8(pack(a - f.x, b - f.y));
+                        }
+                    }
+            }
+
+            // ---- O^T += V^T P^T: two halves of 16 tokens -------------------
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                uint4 v[4];   // codes 16r .. 16r + 15 of tokens 2q, 2q + 1, 2q + 8, 2q + 9
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int row = 16 * m + 2 * q + (k & 1) + 8 * (k >> 1);
+                    v[k] = lds128(vb + row * kHeadDim + ((r ^ (row & 7)) << 4));
+                }
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t t0 = w == 0 ? v[0].x : w == 1 ? v[0].y : w == 2 ? v[0].z : v[0].w;
+                    const uint32_t t1 = w == 0 ? v[1].x : w == 1 ? v[1].y : w == 2 ? v[1].z : v[1].w;
+                    const uint32_t t2 = w == 0 ? v[2].x : w == 1 ? v[2].y : w == 2 ? v[2].z : v[2].w;
+                    const uint32_t t3 = w == 0 ? v[3].x : w == 1 ? v[3].y : w == 2 ? v[3].z : v[3].w;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t sel = half ? 0x7362 : 0x5140;   // the two tokens' codes side by side
+                        const uint32_t x = Codes<CODE>::bias(__byte_perm(t0, t1, sel));
+                        const uint32_t y = Codes<CODE>::bias(__byte_perm(t2, t3, sel));
+                        const uint32_t a[4] = {Codes<CODE>::lo(x), Codes<CODE>::hi(x), Codes<CODE>::lo(y), Codes<CODE>::hi(y)};
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int z = 0; z < PARTS; ++z) mma16816(o[n][2 * w + half], a, pf[z][n][m][0], pf[z][n][m][1]);
+                    }
+                }
+            }
+            __syncwarp();   // the stage may be filled again
+
+            // ---- end of an item, or of this warp's share -------------------
+            const bool last = at.step + 1 == at.r.steps;
+            if (last || i + 1 == left) {
+                const bool whole_item = last && first_step == 0;
+                const int slot = s_part[warp][0].id < 0 && first_step != 0 ? 0 : 1;
+                float den[NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float s = l[n][c];
+                        s += __shfl_xor_sync(0xffffffffu, s, 4);
+                        s += __shfl_xor_sync(0xffffffffu, s, 8);
+                        s += __shfl_xor_sync(0xffffffffu, s, 16);
+                        den[n][c] = s;
+                    }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        int token, head;
+                        const int row = n * 8 + 2 * q + c;
+                        if (!row_of(p, at.r, at.item, at.tiles, row, &token, &head)) continue;
+                        float v[16];
+#pragma unroll
+                        for (int m = 0; m < 8; ++m) {
+                            v[2 * m] = o[n][m][c];
+                            v[2 * m + 1] = o[n][m][c + 2];
+                        }
+                        if (whole_item) {
+                            const float d = den[n][c];
+                            const float inv = d > 0.f ? __fdiv_rn(1.f, d) : (d == 0.f ? 0.f : d);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) v[k] *= inv;
+                            store_out<F32>(p, ((int64_t)(at.r.first + token) * p.kv_heads * p.g + head) * kHeadDim + 16 * r, v, 16);
+                        } else {
+                            const int64_t k = (int64_t)(my_parts + slot) * R + row;
+                            float4* to = reinterpret_cast<float4*>(p.part + k * kHeadDim + 16 * r);
+#pragma unroll
+                            for (int m = 0; m < 4; ++m)
+                                to[m] = make_float4(v[4 * m], v[4 * m + 1], v[4 * m + 2], v[4 * m + 3]);
+                            if (r == 0) *reinterpret_cast<float2*>(p.ml + k * 2) = make_float2(M[n][c], den[n][c]);
+                        }
+                    }
+                if (!whole_item && lane == 0)
+                    s_part[warp][slot] = Part{((int64_t)at.b << 32) | (uint32_t)at.item, first_step == 0, last};
+                __syncwarp();
+                if (i + 1 < left) {
+                    at.next(p);
+                    first_step = 0;
+                    begin();
+                }
+            } else {
+                ++at.step;
+            }
+        }
+        cp_wait<0>();
+    }
+
+    // ---- items that several warps of this CTA share ------------------------
+    __syncthreads();
+    if (t < kMeta) p.meta[cta * kMeta + t] = 0;
+    __syncthreads();
+    int i = 0;
+    while (i < 2 * kWarps) {
+        const Part a = s_part[i >> 1][i & 1];
+        if (a.id < 0) {
+            ++i;
+            continue;
+        }
+        int list[2 * kWarps], n = 0, end = i, ends = 0;
+        while (end < 2 * kWarps) {
+            const Part z = s_part[end >> 1][end & 1];
+            if (z.id >= 0) {
+                if (z.id != a.id) break;
+                list[n++] = end;
+                ends = z.ends;
+            }
+            ++end;
+        }
+        const int b = (int)(a.id >> 32), item = (int)(uint32_t)a.id;
+        const int to = a.begins && ends ? -1 : cta * kPartsPerCta + 2 * kWarps + (a.begins ? 1 : 0);
+        join<R, F32>(p, n, [&](int k) { return cta * kPartsPerCta + list[k]; }, to, b, item);
+        if (t == 0 && to >= 0) {
+            int* m = p.meta + cta * kMeta;
+            if (!a.begins) {
+                m[0] = ends;
+            } else {
+                m[1] = 1;
+                m[2] = b;
+                m[3] = item;
+            }
+        }
+        i = end;
+    }
+}
+
+// Items that several CTAs share: CTA c joins the one that its partial 1 begins
+// with the partials 0 of the CTAs after it, up to the one that ends it.
+template <int NT, bool F32>
+__global__ void __launch_bounds__(256) q8_join_kernel(const AttnArgs p) {
+    constexpr int R = 8 * NT;
+    const int cta = blockIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int* m = p.meta + cta * kMeta;
+    if (m[1] == 0) return;
+    __shared__ int s_n;
+    if (threadIdx.x < 32) {   // how many CTAs follow
+        int n = 0;
+        for (int c0 = cta + 1; c0 < p.ctas; c0 += 32) {
+            const int c = c0 + (int)threadIdx.x;
+            const bool e = c < p.ctas && p.meta[c * kMeta] != 0;
+            const uint32_t hit = __ballot_sync(0xffffffffu, e);
+            if (hit) {
+                n += __ffs(hit);
+                break;
+            }
+            n += 32;
+        }
+        if (threadIdx.x == 0) s_n = min(n, p.ctas - 1 - cta);
+    }
+    __syncthreads();
+    join<R, F32>(p, 1 + s_n,
+                 [&](int k) { return (cta + k) * kPartsPerCta + 2 * kWarps + (k == 0 ? 1 : 0); }, -1, m[2], m[3]);
+}
+
+template <int CODE, int NT, bool F32, bool MOD>
+cudaError_t run(const AttnArgs& a, cudaStream_t s) {
+    static SmemOnce once;
+    cudaError_t e = once.set(q8_rows_kernel<CODE, NT, F32, MOD>, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    q8_rows_kernel<CODE, NT, F32, MOD><<<a.ctas, kThreads, kSmemBytes, s>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.ctas);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, q8_join_kernel<NT, F32>, a);
+}
+
+template <int CODE, bool F32, bool MOD>
+cudaError_t by_tiles(const AttnArgs& a, int tiles8, cudaStream_t s) {
+    return tiles8 == 1 ? run<CODE, 1, F32, MOD>(a, s) : run<CODE, 2, F32, MOD>(a, s);
+}
+
+template <int CODE>
+cudaError_t by_type(const AttnArgs& a, bool f32, int tiles8, cudaStream_t s) {
+    const bool mod = a.cap > 0.f || a.slopes != nullptr;
+    if (f32) return mod ? by_tiles<CODE, true, true>(a, tiles8, s) : by_tiles<CODE, true, false>(a, tiles8, s);
+    return mod ? by_tiles<CODE, false, true>(a, tiles8, s) : by_tiles<CODE, false, false>(a, tiles8, s);
+}
+
+}  // namespace
+
+cudaError_t launch_q8_rows(const AttnArgs& a, int code, bool f32, int tiles8, cudaStream_t s) {
+    return code == ISKV_CODE_INT8 ? by_type<ISKV_CODE_INT8>(a, f32, tiles8, s)
+                                  : by_type<ISKV_CODE_E4M3>(a, f32, tiles8, s);
+}
+
+}  // namespace q8
+}  // namespace iskv

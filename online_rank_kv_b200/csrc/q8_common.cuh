@@ -1,0 +1,181 @@
+// Shared pieces of the paged 8-bit cache (iskv_page_plan, iskv_q8_append,
+// iskv_q8_attention): launch descriptors, code conversions, small scans.
+#pragma once
+
+#include <atomic>
+
+#include "iskv_internal.cuh"
+
+namespace iskv {
+namespace q8 {
+
+constexpr int kPage = ISKV_PAGE;      // tokens per page
+constexpr int kMaxBatch = 8192;       // requests per call
+constexpr int kStepTokens = 32;       // tokens a warp of the split kernel takes at a time
+constexpr float kMinAmax = 5.421010862427522e-20f;   // 2^-64: below it a block counts as zeros
+constexpr float kLog2e = 1.4426950408889634f;
+// Softmax weights are kept times 2^kWeightShift, so that their 16-bit form
+// stays clear of fp16's subnormal range down to 2^-28 of the largest one.
+constexpr float kWeightShift = 14.f;
+
+// Raises a kernel's dynamic shared memory limit once per device instead of at
+// every launch (launch latency is most of a small call).
+struct SmemOnce {
+    std::atomic<uint64_t> done{0};
+    template <typename F>
+    cudaError_t set(F* kernel, size_t bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+        if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
+
+struct AppendArgs {
+    const void* x[2];          // k, v
+    int64_t stride[2];         // elements from token to token
+    void* store[2];
+    float* scale[2];
+    const int32_t* slots;
+    int32_t* status;
+    int64_t n;
+    int pages, kv_heads;
+    int window;                // tokens whose runs one CTA looks after
+};
+
+struct AttnArgs {
+    const void* q;
+    void* out;
+    const uint8_t* k;
+    const uint8_t* v;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* cu;
+    const int32_t* prefix;
+    const float* slopes;
+    int64_t tokens, q_stride;
+    int batch, width, pages, kv_heads, g;
+    int window;
+    float scale, cap;
+    int tq;                    // query tokens per row tile
+    int ctas;                  // CTAs of the split kernel
+    float* part;               // partial results of warps and CTAs
+    float* ml;                 // their running maxima and sums
+    int* meta;                 // per CTA: what it leaves to be joined
+};
+
+// ---------------------------------------------------------------------------
+// Codes to fp16, two at a time, exactly.
+// ---------------------------------------------------------------------------
+template <int CODE>
+struct Codes;
+
+template <>
+struct Codes<ISKV_CODE_INT8> {
+    // 1024 + (c + 128) is an fp16 whose low byte is c with its top bit
+    // flipped; subtracting 1152 leaves c.
+    static __device__ __forceinline__ uint32_t bias(uint32_t x) { return x ^ 0x80808080u; }
+    static __device__ __forceinline__ uint32_t sub(uint32_t x) {
+        const __half2 k = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+        const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), k);
+        return *reinterpret_cast<const uint32_t*>(&r);
+    }
+    static __device__ __forceinline__ uint32_t lo(uint32_t biased) {
+        return sub(__byte_perm(biased, 0x64646464u, 0x4140));
+    }
+    static __device__ __forceinline__ uint32_t hi(uint32_t biased) {
+        return sub(__byte_perm(biased, 0x64646464u, 0x4342));
+    }
+};
+
+template <>
+struct Codes<ISKV_CODE_E4M3> {
+    static __device__ __forceinline__ uint32_t bias(uint32_t x) { return x; }
+    static __device__ __forceinline__ uint32_t cvt(uint16_t x) {
+        uint32_t r;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t lo(uint32_t x) { return cvt((uint16_t)(x & 0xffffu)); }
+    static __device__ __forceinline__ uint32_t hi(uint32_t x) { return cvt((uint16_t)(x >> 16)); }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// tanh(x) = 1 - 2 / (1 + e^(2x)): absolute error a few 2^-23 for every x, and
+// exact limits at both ends (e^(2x) reaches 0 and infinity).
+__device__ __forceinline__ float tanh_abs(float x) {
+    return 1.f - __fdividef(2.f, 1.f + ex2(2.f * kLog2e * x));
+}
+
+// ---------------------------------------------------------------------------
+// What a request's queries see, in steps of `kStep` tokens.
+// ---------------------------------------------------------------------------
+template <int kStep>
+struct Seen {
+    int first, n, len;      // first query row, queries, stored tokens
+    int pre;                // prefix tokens (0 .. len)
+    int a, lo;              // steps 0 .. a-1 and from lo on hold what is seen
+    int steps;              // number of them
+    __device__ __forceinline__ int step_of(int i) const { return i < a ? i : i - a + lo; }
+};
+
+template <int kStep>
+__device__ __forceinline__ Seen<kStep> seen_of(const AttnArgs& p, int b) {
+    Seen<kStep> r;
+    const int c0 = p.cu[b];
+    const int64_t c1 = p.cu[b + 1];
+    const int64_t top = c1 < p.tokens ? c1 : p.tokens;
+    r.first = c0 < 0 ? 0 : c0;
+    r.n = top > r.first ? (int)(top - r.first) : 0;
+    int64_t len = p.lens[b];
+    const int64_t room = (int64_t)p.width * kPage;
+    len = len < 0 ? 0 : (len > room ? room : len);
+    r.len = (int)len;
+    r.pre = 0;
+    if (p.prefix) {
+        const int f = p.prefix[b];
+        r.pre = f < 0 ? 0 : (f > r.len ? r.len : f);
+    }
+    r.a = 0;
+    r.lo = 0;
+    if (p.window > 0) {
+        int64_t w0 = (int64_t)r.len - r.n - p.window + 1;   // first key the first query sees
+        if (w0 < 0) w0 = 0;
+        r.lo = (int)(w0 / kStep);
+        r.a = (r.pre + kStep - 1) / kStep;
+        if (r.a > r.lo) r.a = r.lo;
+    }
+    const int end = (r.len + kStep - 1) / kStep;
+    r.steps = r.a + (end > r.lo ? end - r.lo : 0);
+    if (r.n == 0) r.steps = 0;
+    else if (r.steps == 0) r.steps = 1;   // nothing stored: one empty step, so that zeros are written
+    return r;
+}
+
+cudaError_t launch_page_plan(const iskv_page_plan_args& a, cudaStream_t s);
+cudaError_t launch_q8_append(const AppendArgs& a, int code, int dtype, cudaStream_t s);
+cudaError_t launch_q8_rows(const AttnArgs& a, int code, bool f32, int tiles8, cudaStream_t s);
+
+// floats of workspace of the split kernel for `ctas` CTAs and row tiles of
+// 8 * tiles8 rows: per CTA two partials of every warp and two of its own
+constexpr int kRowWarps = 8;
+constexpr int kPartsPerCta = 2 * kRowWarps + 2;
+
+}  // namespace q8
+}  // namespace iskv
