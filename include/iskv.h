@@ -491,6 +491,8 @@ ISKV_API int iskv_q8_append(const iskv_q8_pages* store, const void* k, const voi
  * The workspace (iskv_q8_workspace bytes, 16-byte aligned, any contents)
  * belongs to the call until the stream has passed it: calls that may overlap
  * need one each.
+ * *status is set to ISKV_ERR_DEVICE_TIMEOUT where a bounded wait inside the
+ * kernel gave up (out is then incomplete) and is otherwise left.
  * q_heads / kv_heads <= 8; ISKV_BF16 or ISKV_F32 queries; q, out and
  * workspace 16-byte aligned, q_stride a multiple of 16 bytes.
  * Errors: INVALID_ARG, UNSUPPORTED (head_dim, page, heads per group),
@@ -515,6 +517,7 @@ typedef struct {
     const float* slopes;        /* [q_heads], or NULL                        */
     void* workspace;
     int64_t workspace_bytes;
+    int32_t* status;            /* [1], sticky, or NULL                      */
 } iskv_q8_attention_args;
 
 ISKV_API int iskv_q8_attention(const iskv_q8_pages* store, const iskv_q8_attention_args* args,

@@ -108,7 +108,7 @@ class _Q8Attention(ctypes.Structure):
         (n, ctypes.c_float) for n in ("scale", "cap")] + [
         (n, ctypes.c_int64) for n in ("tokens", "q_stride")] + [
         (n, ctypes.c_void_p) for n in ("q", "out", "table", "lens", "cu", "prefix", "slopes", "workspace")] + [
-        ("workspace_bytes", ctypes.c_int64)]
+        ("workspace_bytes", ctypes.c_int64), ("status", ctypes.c_void_p)]
 
 
 _vp, _i, _i64p = ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(ctypes.c_int64)
@@ -520,7 +520,7 @@ class Q8Pages:
                             out.data_ptr(), _int32(dev, (batch, width), table, "table"),
                             _int32(dev, (batch,), lens, "lens"), _int32(dev, (batch + 1,), cu, "cu"),
                             None if prefix is None else _int32(dev, (batch,), prefix, "prefix"),
-                            None if slopes is None else slopes.data_ptr(), ws.data_ptr(), need)
+                            None if slopes is None else slopes.data_ptr(), ws.data_ptr(), need, self._status.data_ptr())
         if stream is not None:   # the workspace comes from the current stream's pool
             ws.record_stream(stream)
         _launch(dev, LIB.iskv_q8_attention, "iskv_q8_attention", ctypes.byref(self._c), ctypes.byref(args),
@@ -528,7 +528,7 @@ class Q8Pages:
         return out
 
     def status(self) -> int:
-        """Synchronize and return the sticky status of the appends: 0, or the
-        code of non-finite rows (RANGE) or slots outside the pool
-        (INVALID_ARG)."""
+        """Synchronize and return the sticky status of the calls on these pages:
+        0, or the smallest code of non-finite rows (RANGE), a device-side wait
+        that gave up (DEVICE_TIMEOUT) and slots outside the pool (INVALID_ARG)."""
         return int(self._status.item())

@@ -64,6 +64,14 @@ int64_t rows_floats(int ctas, int tiles8) {
     return (int64_t)ctas * q8::kPartsPerCta * 8 * tiles8 * (kHeadDim + 2);
 }
 
+int64_t prompt_floats(int ctas) { return (int64_t)ctas * 2 * q8::kPromptRows * (kHeadDim + 2); }
+
+// Query rows per KV head from which a request is a prompt: the tcgen05 kernel
+// works on 256 rows at a time, the split kernel on 8 or 16.
+constexpr int64_t kPromptMinRows = 32;
+
+bool is_prompt(int g, int max_new, int dtype) { return dtype == ISKV_BF16 && (int64_t)max_new * g > kPromptMinRows; }
+
 }  // namespace
 
 extern "C" {
@@ -126,7 +134,9 @@ int64_t iskv_q8_workspace(int32_t q_heads, int32_t kv_heads, int64_t tokens, int
         max_new < 1 || (dtype != ISKV_F32 && dtype != ISKV_BF16))
         return -1;
     const int ctas = sm_count();
-    return rows_floats(ctas, row_tiles8(q_heads / kv_heads, max_new)) * 4 + (int64_t)ctas * 16;
+    const int g = q_heads / kv_heads;
+    if (is_prompt(g, max_new, dtype)) return prompt_floats(ctas) * 4 + (int64_t)ctas * q8::kMetaBytes;
+    return rows_floats(ctas, row_tiles8(g, max_new)) * 4 + (int64_t)ctas * q8::kMetaBytes;
 }
 
 int iskv_q8_attention(const iskv_q8_pages* store, const iskv_q8_attention_args* a, void* stream) {
@@ -143,14 +153,14 @@ int iskv_q8_attention(const iskv_q8_pages* store, const iskv_q8_attention_args* 
     if (a->batch == 0 || a->tokens == 0) return ISKV_OK;
     if (!a->q || !a->out || !a->table || !a->lens || !a->cu || !a->workspace) return ISKV_ERR_INVALID_ARG;
     if (!aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->workspace, 16) || !aligned(a->table, 4) ||
-        !aligned(a->lens, 4) || !aligned(a->cu, 4) || !aligned(a->prefix, 4) || !aligned(a->slopes, 4))
+        !aligned(a->lens, 4) || !aligned(a->cu, 4) || !aligned(a->prefix, 4) || !aligned(a->slopes, 4) || !aligned(a->status, 4))
         return ISKV_ERR_INVALID_ARG;
     if (a->q_stride % (16 / elem_bytes(a->dtype)) != 0 ||
         (a->tokens > 1 && a->q_stride < (int64_t)a->q_heads * kHeadDim))
         return ISKV_ERR_INVALID_ARG;
     const void* ptrs[] = {store->k, store->v, store->k_scale, store->v_scale, a->q, a->out, a->table, a->lens, a->cu,
-                          a->prefix, a->slopes, a->workspace};
-    if (!all_on_device(ptrs, 12)) return ISKV_ERR_INVALID_ARG;
+                          a->prefix, a->slopes, a->workspace, a->status};
+    if (!all_on_device(ptrs, 13)) return ISKV_ERR_INVALID_ARG;
     if (a->workspace_bytes < iskv_q8_workspace(a->q_heads, store->kv_heads, a->tokens, a->max_new, a->dtype))
         return ISKV_ERR_CAPACITY;
     q8::AttnArgs p{};
@@ -177,12 +187,16 @@ int iskv_q8_attention(const iskv_q8_pages* store, const iskv_q8_attention_args* 
     p.cap = a->cap;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int tiles8 = row_tiles8(g, a->max_new);
-    p.tq = 8 * tiles8 / g;
+    const bool prompt = is_prompt(g, a->max_new, a->dtype);
+    p.tq = (prompt ? q8::kPromptRows / 2 : 8 * tiles8) / g;
     p.ctas = sm_count();
-    const int64_t parts = (int64_t)p.ctas * q8::kPartsPerCta * 8 * tiles8;
+    const int64_t parts = (int64_t)p.ctas * (prompt ? 2 * q8::kPromptRows : q8::kPartsPerCta * 8 * tiles8);
     p.part = static_cast<float*>(a->workspace);
     p.ml = p.part + parts * kHeadDim;
     p.meta = reinterpret_cast<int*>(p.ml + parts * 2);
+    p.status = a->status;
+    if (prompt)
+        return q8::launch_q8_prompt(p, store->code, s) == cudaSuccess ? ISKV_OK : ISKV_ERR_CUDA;
     return q8::launch_q8_rows(p, store->code, a->dtype == ISKV_F32, tiles8, s) == cudaSuccess ? ISKV_OK : ISKV_ERR_CUDA;
 }
 

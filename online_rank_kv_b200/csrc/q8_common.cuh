@@ -67,6 +67,7 @@ struct AttnArgs {
     int ctas;                  // CTAs of the split kernel
     float* part;               // partial results of warps and CTAs
     float* ml;                 // their running maxima and sums
+    int* status;               // sticky, or nullptr
     int* meta;                 // per CTA: what it leaves to be joined
 };
 
@@ -170,12 +171,16 @@ __device__ __forceinline__ Seen<kStep> seen_of(const AttnArgs& p, int b) {
 
 cudaError_t launch_page_plan(const iskv_page_plan_args& a, cudaStream_t s);
 cudaError_t launch_q8_append(const AppendArgs& a, int code, int dtype, cudaStream_t s);
+cudaError_t launch_q8_prompt(const AttnArgs& a, int code, cudaStream_t s);
 cudaError_t launch_q8_rows(const AttnArgs& a, int code, bool f32, int tiles8, cudaStream_t s);
 
 // floats of workspace of the split kernel for `ctas` CTAs and row tiles of
 // 8 * tiles8 rows: per CTA two partials of every warp and two of its own
 constexpr int kRowWarps = 8;
 constexpr int kPartsPerCta = 2 * kRowWarps + 2;
+
+constexpr int kPromptRows = 256;   // query rows that the prompt kernel takes together
+constexpr int kMetaBytes = 32;     // per CTA, either kernel
 
 }  // namespace q8
 }  // namespace iskv
