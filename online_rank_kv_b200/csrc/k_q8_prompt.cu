@@ -13,21 +13,24 @@
 //   warps 0-3, 4-7  softmax of tile 0 and of tile 1, one thread per row: scores
 //                   from TMEM, weights as fp16 back over them, and the rare
 //                   rescaling; also load, scale and store their own Q rows
-//   warps 8-11      turn the codes of K and V tiles into fp16 operands (global
-//                   memory -> registers one tile ahead -> swizzled shared memory)
+//   warps 8-11      turn codes (shared memory) into fp16 operand tiles
 //   warp 12         one thread issues every MMA: S_i = Q_i K^T, O_i += P_i V
+//   warp 13         walks the CTA's work, looks up pages and scales 16 tiles at
+//                   a time, tells the others about each tile through a ring of
+//                   four descriptions, and copies its codes in (8 KB per page
+//                   and operand by the bulk copy engine)
 // While one tile's softmax runs, the other tile's two products do.  TMEM: S_0,
 // S_1 (fp32, the fp16 weights over their first half), O_0, O_1, 128 columns
-// each.  K and V tiles have two buffers each.
+// each.  K and V operand tiles have two buffers each, codes one.
 //
 // Work: (KV head, pair of query tiles, key tile) are numbered through and every
 // CTA takes an equal contiguous range, so that causal triangles, ragged batches
 // and short chunks on long caches all fill the GPU; a pair that crosses CTAs is
 // joined from its partial sums by a second kernel.
 //
-// Bounds per key tile and pair (148 SMs at 1.85 GHz): 2048 cycles of MMA, 2048
-// cycles of exponentials (16 per SM and clock), about 1500 issue slots per
-// scheduler.
+// Bounds per key tile and pair (148 SMs): 2048 cycles of MMA (64 per
+// instruction, measured alone), 2048 cycles of exponentials (16 per SM and
+// clock).
 #include "q8_common.cuh"
 #include "tc_util.cuh"
 
@@ -41,11 +44,32 @@ constexpr int kN = 128;                    // keys per tile
 constexpr int kTileBytes = kN * kHeadDim * 2;   // one fp16 operand tile: 32 KB
 constexpr int kHalf = kTileBytes / 2;      // 64 of its 128 columns: rows of 128 bytes
 constexpr int kSoftmaxWarps = 8, kCodeWarps = 4;
-constexpr int kThreads = 32 * (kSoftmaxWarps + kCodeWarps + 1);
+// Registers per thread, by warpgroup: 2 x 176 + 80 + 80 = 4 x 128, what the
+// launch has.
+constexpr int kThreads = 32 * (kSoftmaxWarps + kCodeWarps + 4);
+constexpr int kSoftmaxRegs = 176, kCodeRegs = 80, kOtherRegs = 80;
+constexpr int kMmaWarp = kSoftmaxWarps + kCodeWarps, kWalkWarp = kMmaWarp + 1;
 constexpr float kShift = 7.f;
 constexpr float kRaise = 8.f;
+// What the start and the end of a pair cost, in key tiles, where work is split.
+constexpr int kPieceTiles = 3;
+
+// One key tile, as the walking warp describes it.
+constexpr int kFirst = 1, kLast = 2, kEnd = 4;   // of a piece; of the work
+struct Tile {
+    int flags, key0;
+    int there[2];           // its pages exist
+    float sk[2], lsv[2], isv[2];   // key scale, log2 of the value scale, its inverse
+    int len, pre, n, first; // the request: tokens, prefix, queries, first query row
+    int token0, h;          // the pair's first query, KV head
+    int slot;               // partial slot, -1: the piece is the whole pair
+};
+constexpr int kTiles = 4;
 
 struct Shared {
+    Tile tile[kTiles];
+    uint64_t info_full[kTiles], info_empty[kTiles];
+    uint64_t kc_full, kc_empty, vc_full, vc_empty;
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t q_full, s_full[2], p_full[2], pv_done[2], drain;
     uint32_t tmem;
@@ -54,8 +78,18 @@ struct Shared {
     int64_t start_off;
     int start_b, start_pair;
 };
-// dynamic shared memory: 1024-byte aligned [K 2 tiles][V 2 tiles][Q 2 tiles]
-constexpr int kSmemBytes = 6 * kTileBytes + 1024;
+constexpr int kCodeBytes = kN * kHeadDim;   // K or V codes of a tile: 16 KB
+// dynamic shared memory: 1024-byte aligned [K 2 tiles][V 2 tiles][Q 2 tiles][K codes][V codes]
+constexpr int kSmemBytes = 6 * kTileBytes + 2 * kCodeBytes + 1024;
+
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
     asm volatile(
@@ -68,18 +102,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
           "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
-        "%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-        : "memory");
-}
-
 // Shared-memory operand with 128-byte rows, 128-byte swizzle (the 16-byte chunk
 // c of row t stands at chunk c ^ (t & 7)).  K-major (Q, K): sbo = 1024 between
 // groups of 8 rows.  MN-major (V, whose rows are the reduction index): sbo =
@@ -136,17 +158,23 @@ __device__ __forceinline__ int pairs_of(const AttnArgs& p, int b) {
     return c1 > c0 ? (int)((c1 - c0 + 2 * p.tq - 1) / (2 * p.tq)) : 0;
 }
 
-// A CTA's run through (head, request, pair, tile).
+// A CTA's run through (head, request, pair, tile).  A pair costs its tiles and
+// kPieceTiles, which stand in front of them.
 struct Walk {
     int h, b, pair, pairs;
     int t0, t1;             // key tiles of the present piece: [t0, t1) of span.tiles
-    int64_t left;           // tiles still to do, this piece's included
+    int64_t left;           // cost still to spend, this piece's included
     Seen<kN> r;
     Span span;
-    __device__ __forceinline__ void cut() {
-        t1 = (int)(left < span.tiles - t0 ? t0 + left : span.tiles);
+    // the piece from cost offset `off` of the pair on; false: no tile of it is this CTA's
+    __device__ __forceinline__ bool cut(int64_t off) {
+        const int64_t end = off + left - kPieceTiles;
+        t0 = off > kPieceTiles ? (int)(off - kPieceTiles) : 0;
+        t1 = (int)(end < span.tiles ? end : span.tiles);
+        left -= span.tiles + kPieceTiles - off;
+        return t1 > t0;
     }
-    __device__ __forceinline__ void start(const AttnArgs& p, int h_, int b_, int pair_, int tile, int64_t n) {
+    __device__ __forceinline__ bool start(const AttnArgs& p, int h_, int b_, int pair_, int64_t off, int64_t n) {
         h = h_;
         b = b_;
         pair = pair_;
@@ -154,11 +182,9 @@ struct Walk {
         r = seen_of<kN>(p, b);
         pairs = pairs_of(p, b);
         span = span_of(p, r, pair);
-        t0 = tile;
-        cut();
+        return cut(off);
     }
     __device__ __forceinline__ bool next(const AttnArgs& p) {
-        left -= t1 - t0;
         if (left <= 0) return false;
         if (++pair == pairs) {
             pair = 0;
@@ -172,11 +198,8 @@ struct Walk {
             r = seen_of<kN>(p, b);
         }
         span = span_of(p, r, pair);
-        t0 = 0;
-        cut();
-        return true;
+        return cut(0);
     }
-    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == span.tiles; }
 };
 
 // bits lo .. hi-1 of 32 (clipped)
@@ -191,6 +214,450 @@ __device__ __forceinline__ uint32_t bits(int lo, int hi) {
 // [1] its partial 1 begins one; [2] request, [3] KV head, [4] pair.
 constexpr int kMeta = 8;
 
+// =================== softmax: one thread per row ============================
+template <bool MOD>
+__device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint8_t* sQ, uint32_t tmem, int warp, int lane) {
+    const int i = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t quad = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + i * kN + quad, tO = tmem + 2 * kN + i * kHeadDim + quad;
+    const int k = row / p.g, hg = row % p.g;
+    float rowf = 0.f, slope = 0.f, M = -INFINITY, l = 0.f;
+    int pos = 0, see_from = -1, token = 0, head = 0;
+    int wp_min = 0, wp_max = 0;
+    bool on = false;
+
+    for (int n = 0;; ++n) {
+        const Tile& ti = sh.tile[n % kTiles];
+        bool ok = wait_for(sh, &sh.info_full[n % kTiles], (n / kTiles) & 1);
+        const int flags = ok ? ti.flags : kEnd;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok || (flags & kEnd)) return;
+
+        if (flags & kFirst) {   // this row's query
+            token = ti.token0 + i * p.tq + k;
+            head = ti.h * p.g + hg;
+            on = k < p.tq && token < ti.n;
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                              (int64_t)(ti.first + (on ? token : 0)) * p.q_stride +
+                                                              head * kHeadDim);
+            uint4 x[16];
+            float top = 0.f;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) x[c] = on ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xffff0000u))));
+            }
+            int up = 14 - ((int)(__float_as_uint(top) >> 23) - 127);
+            up = max(-126, min(126, up));
+            const float f = __uint_as_float((uint32_t)(up + 127) << 23);
+            rowf = __uint_as_float((uint32_t)(127 - up) << 23) * (p.scale * (MOD ? 1.f : kLog2e));
+            uint8_t* q_row = sQ + i * kTileBytes + row * 128;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const __half2 hh = __floats2half2_rn(__uint_as_float(v[e] << 16) * f,
+                                                         __uint_as_float(v[e] & 0xffff0000u) * f);
+                    o[e] = *reinterpret_cast<const uint32_t*>(&hh);
+                }
+                *reinterpret_cast<uint4*>(q_row + (c >> 3) * kHalf + (((c & 7) ^ (row & 7)) << 4)) =
+                    make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            tc::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sh.q_full);
+            pos = ti.len - ti.n + min(token, ti.n - 1);
+            see_from = p.window > 0 ? max(-1, pos - p.window) : -1;   // sees (see_from, pos] and the prefix
+            if (MOD) slope = p.slopes && on ? p.slopes[head] * kLog2e : 0.f;
+            wp_min = __reduce_min_sync(0xffffffffu, pos);
+            wp_max = __reduce_max_sync(0xffffffffu, pos);
+            M = -INFINITY;
+            l = 0.f;
+        }
+
+        const int key0 = ti.key0, len = ti.len, pre = ti.pre;
+        const bool clear = ti.there[0] && ti.there[1] && key0 + kN <= len &&
+                           ((key0 + kN - 1 <= wp_min && (p.window == 0 || key0 > wp_max - p.window)) || key0 + kN <= pre);
+        // the smallest normal number in place of zero keeps hidden scores at -inf
+        float a0 = fmaxf(rowf * ti.sk[0], 1.17549435e-38f), a1 = fmaxf(rowf * ti.sk[1], 1.17549435e-38f);
+        ok = __all_sync(0xffffffffu, wait_for(sh, &sh.s_full[i], n & 1));
+        if (!ok) return;
+        tc::tc_fence_after();
+        uint32_t s[kN];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
+        tc::tmem_wait_ld();
+        if (MOD) {
+            const float d0 = (float)(pos - key0);
+#pragma unroll
+            for (int e = 0; e < kN; ++e) {
+                float x = __uint_as_float(s[e]) * (e < kPage ? a0 : a1);
+                if (p.cap > 0.f) x = p.cap * tanh_abs(__fdividef(x, p.cap));
+                s[e] = __float_as_uint(x * kLog2e - slope * fabsf(d0 - (float)e));
+            }
+            a0 = a1 = 1.f;
+        }
+        if (!clear) {
+            const bool there0 = ti.there[0], there1 = ti.there[1];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int k0 = key0 + 32 * c;
+                uint32_t m = (bits(see_from + 1 - k0, pos + 1 - k0) | bits(0, pre - k0)) & bits(0, len - k0);
+                if (!(c < 2 ? there0 : there1)) m = 0u;
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (!((m >> e) & 1u)) s[32 * c + e] = 0xff800000u;   // -inf
+            }
+        }
+        // ---- the row's maximum ----
+        float t0 = -INFINITY, t1 = -INFINITY;
+        {
+            float m[8];
+#pragma unroll
+            for (int z = 0; z < 8; ++z) m[z] = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < kN; e += 2) {
+                const int z = (e >> 1) & 3;
+                float& r = m[e < kPage ? z : 4 + z];
+                r = fmaxf(r, fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
+            }
+            t0 = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+            t1 = fmaxf(fmaxf(m[4], m[5]), fmaxf(m[6], m[7]));
+        }
+        const float lsv0 = ti.lsv[0], lsv1 = ti.lsv[1];
+        const float now = fmaxf(fmaf(t0, a0, lsv0), fmaf(t1, a1, lsv1));
+        const bool raise = now > M + kRaise || (M == -INFINITY && now > -INFINITY);
+        if (__any_sync(0xffffffffu, raise)) {
+            const float f = raise && M > -INFINITY ? ex2(M - now) : 1.f;
+            if (raise) M = now;
+            l *= f;
+            if (!(flags & kFirst)) {   // the accumulator holds earlier tiles
+                ok = __all_sync(0xffffffffu, wait_for(sh, &sh.pv_done[i], (n - 1) & 1));
+                if (!ok) return;
+                tc::tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t o[16];
+                    tc::tmem_ld16(tO + 16 * c, o);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                    tc::tmem_st16(tO + 16 * c, o);
+                }
+            }
+        }
+        // ---- weights ----
+        // One fused multiply-add per weight: x - M with x unrounded, M and
+        // M - log2 s_v rounded, off by 2^-24 |M| between pages.  Beyond
+        // |M| = 2^10 x is rounded like M was, so that the row's largest key
+        // gives exactly x - M = 0.
+        const float Mb = M == -INFINITY ? 0.f : M;
+        float sum0 = 0.f, sum1 = 0.f;
+        if (__all_sync(0xffffffffu, fabsf(Mb) < 1024.f)) {
+            const float b0 = lsv0 + (kShift - Mb), b1 = lsv1 + (kShift - Mb);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t o[16];
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const float x = ex2(fmaf(__uint_as_float(s[32 * c + e]), c < 2 ? a0 : a1, c < 2 ? b0 : b1));
+                    const float y = ex2(fmaf(__uint_as_float(s[32 * c + e + 1]), c < 2 ? a0 : a1, c < 2 ? b0 : b1));
+                    if (c < 2) sum0 += x + y;
+                    else sum1 += x + y;
+                    const __half2 hh = __floats2half2_rn(x, y);
+                    o[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
+                }
+                tc::tmem_st16(tS + 16 * c, o);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t o[16];
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const float x = ex2((fmaf(__uint_as_float(s[32 * c + e]), c < 2 ? a0 : a1, c < 2 ? lsv0 : lsv1) - Mb) + kShift);
+                    const float y = ex2((fmaf(__uint_as_float(s[32 * c + e + 1]), c < 2 ? a0 : a1, c < 2 ? lsv0 : lsv1) - Mb) + kShift);
+                    if (c < 2) sum0 += x + y;
+                    else sum1 += x + y;
+                    const __half2 hh = __floats2half2_rn(x, y);
+                    o[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
+                }
+                tc::tmem_st16(tS + 16 * c, o);
+            }
+        }
+        l += sum0 * ti.isv[0] + sum1 * ti.isv[1];
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sh.p_full[i]);
+
+        if (flags & kLast) {   // end of the piece
+            ok = __all_sync(0xffffffffu, wait_for(sh, &sh.pv_done[i], n & 1));
+            if (!ok) return;
+            tc::tc_fence_after();
+            const int slot = ti.slot;
+            const int64_t at = (int64_t)slot * (2 * kM) + i * kM + row;
+            const float inv = l > 0.f ? __fdiv_rn(1.f, l) : (l == 0.f ? 0.f : l);
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
+                                 ((int64_t)(ti.first + token) * p.kv_heads * p.g + head) * kHeadDim;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                __syncwarp();
+                tmem_ld32(tO + 32 * c, o);
+                tc::tmem_wait_ld();
+                if (!on) {
+                } else if (slot < 0) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * z]) * inv,
+                                                                            __uint_as_float(o[e + 2 * z + 1]) * inv);
+                            v[z] = *reinterpret_cast<const uint32_t*>(&b2);
+                        }
+                        *reinterpret_cast<uint4*>(out + 32 * c + e) = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                } else {
+                    float4* to = reinterpret_cast<float4*>(p.part + at * kHeadDim + 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        to[e / 4] = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                                __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+                }
+            }
+            if (slot >= 0 && on) *reinterpret_cast<float2*>(p.ml + at * 2) = make_float2(M, l);
+            tc::tc_fence_before();
+            __syncwarp();
+        }
+        if (lane == 0) tc::mbar_arrive(&sh.info_empty[n % kTiles]);
+    }
+}
+
+// =================== codes to operand tiles =================================
+// Per pass 8 threads take a row of 128 codes.  A thread's 16 codes become
+// chunks 2c and 2c + 1 of one 64-column half; threads of the second half store
+// theirs in the other order, which keeps the 8 threads of a row on different
+// banks.
+template <int CODE>
+__device__ __forceinline__ void code_tile(uint8_t* tile, const uint8_t* codes, int u, int rows0, int rows1) {
+    const int c = u & 7, row0 = u >> 3, first = c >> 2, c0 = 2 * (c & 3);
+    uint4 x[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+        const int rr = s * 16 + row0;
+        x[s] = *reinterpret_cast<const uint4*>(codes + rr * kHeadDim + c * 16);
+        if ((rr & (kPage - 1)) >= (s < 4 ? rows0 : rows1)) x[s] = make_uint4(0u, 0u, 0u, 0u);   // behind the last token
+    }
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+        const int rr = s * 16 + row0;
+        uint8_t* to = tile + (c >> 2) * kHalf + rr * 128;
+        const uint32_t v[4] = {Codes<CODE>::bias(x[s].x), Codes<CODE>::bias(x[s].y), Codes<CODE>::bias(x[s].z),
+                               Codes<CODE>::bias(x[s].w)};
+        const uint4 lo = make_uint4(Codes<CODE>::lo(v[0]), Codes<CODE>::hi(v[0]), Codes<CODE>::lo(v[1]), Codes<CODE>::hi(v[1]));
+        const uint4 hi = make_uint4(Codes<CODE>::lo(v[2]), Codes<CODE>::hi(v[2]), Codes<CODE>::lo(v[3]), Codes<CODE>::hi(v[3]));
+        *reinterpret_cast<uint4*>(to + (((c0 + first) ^ (rr & 7)) << 4)) = first ? hi : lo;
+        *reinterpret_cast<uint4*>(to + (((c0 + 1 - first) ^ (rr & 7)) << 4)) = first ? lo : hi;
+    }
+}
+
+template <int CODE>
+__device__ __forceinline__ void code_role(Shared& sh, uint8_t* sK, uint8_t* sV, const uint8_t* sKc, const uint8_t* sVc, int u, int lane) {
+    for (int n = 0;; ++n) {
+        const Tile& ti = sh.tile[n % kTiles];
+        if (!wait_for(sh, &sh.info_full[n % kTiles], (n / kTiles) & 1) || (ti.flags & kEnd)) return;
+        const int rows = ti.len - ti.key0;
+        const int rows0 = ti.there[0] ? min(kPage, rows) : 0, rows1 = ti.there[1] ? min(kPage, rows - kPage) : 0;
+        const int st = n & 1;
+        const uint32_t par = (n >> 1) & 1;
+        if (!wait_for(sh, &sh.kc_full, n & 1) || !wait_for(sh, &sh.k_empty[st], par ^ 1)) return;
+        code_tile<CODE>(sK + st * kTileBytes, sKc, u, rows0, rows1);
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tc::mbar_arrive(&sh.k_full[st]);
+            tc::mbar_arrive(&sh.kc_empty);
+        }
+        if (!wait_for(sh, &sh.vc_full, n & 1) || !wait_for(sh, &sh.v_empty[st], par ^ 1)) return;
+        code_tile<CODE>(sV + st * kTileBytes, sVc, u, rows0, rows1);
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tc::mbar_arrive(&sh.v_full[st]);
+            tc::mbar_arrive(&sh.vc_empty);
+            tc::mbar_arrive(&sh.info_empty[n % kTiles]);
+        }
+    }
+}
+
+// =================== MMA (one thread) =======================================
+__device__ __forceinline__ void mma_role(Shared& sh, const uint8_t* sK, const uint8_t* sV, const uint8_t* sQ, uint32_t tmem) {
+    constexpr uint32_t idS = tc::idesc_f32acc(0, kM, kN, 0, 0), idO = tc::idesc_f32acc(0, kM, kHeadDim, 0, 1);
+    const uint64_t dK = desc_sw128(tc::smem_u32(sK), 16, 1024), dQ = desc_sw128(tc::smem_u32(sQ), 16, 1024);
+    const uint64_t dV = desc_sw128(tc::smem_u32(sV), kHalf, 1024);
+    // descriptors step in units of 16 bytes
+    auto scores = [&](int i, int st) {
+        const uint64_t a = dQ + i * (kTileBytes >> 4), b = dK + st * (kTileBytes >> 4);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int o = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+            tc::mma_f16_ss(tmem + i * kN, a + o, b + o, idS, k > 0);
+        }
+        tc::mma_commit(&sh.s_full[i]);
+    };
+    auto values = [&](int i, int st, uint32_t more) {
+        const uint64_t b = dV + st * (kTileBytes >> 4);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            tc::mma_f16_ts(tmem + 2 * kN + i * kHeadDim, tmem + i * kN + k * 8, b + k * (2048 >> 4), idO, k > 0 ? 1u : more);
+        tc::mma_commit(&sh.pv_done[i]);
+    };
+    int piece = 0;
+    for (int n = 0;; ++n) {
+        if (!wait_for(sh, &sh.info_full[n % kTiles], (n / kTiles) & 1)) break;
+        const int flags = sh.tile[n % kTiles].flags;
+        if (flags & kEnd) break;
+        const int st = n & 1;
+        if (flags & kFirst) {
+            if (!wait_for(sh, &sh.q_full, piece & 1) || !wait_for(sh, &sh.k_full[st], (n >> 1) & 1)) break;
+            ++piece;
+            tc::tc_fence_after();
+            scores(0, st);
+            scores(1, st);
+            tc::mma_commit(&sh.k_empty[st]);
+        }
+        const int nx = n + 1, sx = nx & 1;
+        if (!wait_for(sh, &sh.v_full[st], (n >> 1) & 1) || !wait_for(sh, &sh.p_full[0], n & 1)) break;
+        tc::tc_fence_after();
+        values(0, st, !(flags & kFirst));
+        if (!(flags & kLast)) {
+            if (!wait_for(sh, &sh.k_full[sx], (nx >> 1) & 1)) break;
+            tc::tc_fence_after();
+            scores(0, sx);
+        }
+        if (!wait_for(sh, &sh.p_full[1], n & 1)) break;
+        tc::tc_fence_after();
+        values(1, st, !(flags & kFirst));
+        tc::mma_commit(&sh.v_empty[st]);
+        if (!(flags & kLast)) {
+            scores(1, sx);
+            tc::mma_commit(&sh.k_empty[sx]);
+        }
+        tc::mbar_arrive(&sh.info_empty[n % kTiles]);
+    }
+    // every MMA has ended before tensor memory is given back
+    tc::mma_commit(&sh.drain);
+    tc::mbar_wait(&sh.drain, 0, clock64() + tc::kWaitCycles);
+}
+
+// =================== the walk ===============================================
+__device__ __forceinline__ void walk_role(const AttnArgs& p, Shared& sh, uint8_t* sKc, uint8_t* sVc, int start_h, int64_t left, int lane) {
+    Walk w;
+    bool more = w.start(p, start_h, sh.start_b, sh.start_pair, sh.start_off, left);
+    if (!more) more = w.next(p);
+    int n = 0;
+    bool ok = true;
+    while (ok && more) {
+        const bool begins = w.t0 == 0, ends = w.t1 == w.span.tiles;
+        const int slot = begins && ends ? -1 : (int)blockIdx.x * 2 + (begins ? 1 : 0);
+        if (lane == 0 && slot >= 0) {
+            int* m = p.meta + blockIdx.x * kMeta;
+            if (!begins) {
+                m[0] = ends;
+            } else {
+                m[1] = 1;
+                m[2] = w.b;
+                m[3] = w.h;
+                m[4] = w.pair;
+            }
+        }
+        int page = -1;
+        float sk = 0.f, lsv = 0.f, isv = 1.f;
+        for (int i = w.t0; i < w.t1; ++i, ++n) {
+            const int in = (i - w.t0) & 15;
+            if (in == 0) {   // pages and scales of 16 tiles, a page per lane
+                const int j = i + (lane >> 1);
+                const int tok = w.span.tile_of(j) * kN + (lane & 1) * kPage;
+                page = j < w.t1 && tok < w.r.len ? __ldg(p.table + (int64_t)w.b * p.width + tok / kPage) : -1;
+                if (page >= p.pages) page = -1;
+                const int64_t at = (int64_t)max(page, 0) * p.kv_heads + w.h;
+                sk = page >= 0 ? __ldg(p.k_scale + at) : 0.f;
+                float sv = page >= 0 ? __ldg(p.v_scale + at) : 1.f;
+                if (!(sv > 0.f)) sv = 1.f;   // a block of zeros
+                lsv = lg2(sv);
+                isv = __fdividef(1.f, sv);
+            }
+            const int pg0 = __shfl_sync(0xffffffffu, page, 2 * in), pg1 = __shfl_sync(0xffffffffu, page, 2 * in + 1);
+            ok = wait_for(sh, &sh.info_empty[n % kTiles], ((n / kTiles) & 1) ^ 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            Tile& ti = sh.tile[n % kTiles];
+            if ((lane >> 1) == in) {
+                ti.there[lane & 1] = page >= 0;
+                ti.sk[lane & 1] = sk;
+                ti.lsv[lane & 1] = lsv;
+                ti.isv[lane & 1] = isv;
+            }
+            if (lane == 0) {
+                ti.flags = (i == w.t0 ? kFirst : 0) | (i + 1 == w.t1 ? kLast : 0);
+                ti.key0 = w.span.tile_of(i) * kN;
+                ti.len = w.r.len;
+                ti.pre = w.r.pre;
+                ti.n = w.r.n;
+                ti.first = w.r.first;
+                ti.token0 = w.pair * 2 * p.tq;
+                ti.h = w.h;
+                ti.slot = slot;
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sh.info_full[n % kTiles]);
+            // codes, a page of one operand per copy
+            const uint32_t bytes = (pg0 >= 0 ? kCodeBytes / 2 : 0) + (pg1 >= 0 ? kCodeBytes / 2 : 0);
+            const int64_t a0 = ((int64_t)max(pg0, 0) * p.kv_heads + w.h) * (kCodeBytes / 2);
+            const int64_t a1 = ((int64_t)max(pg1, 0) * p.kv_heads + w.h) * (kCodeBytes / 2);
+            ok = wait_for(sh, &sh.kc_empty, (n & 1) ^ 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) {
+                tc::mbar_arrive_expect_tx(&sh.kc_full, bytes);
+                if (pg0 >= 0) tc::bulk_g2s(sKc, p.k + a0, kCodeBytes / 2, &sh.kc_full);
+                if (pg1 >= 0) tc::bulk_g2s(sKc + kCodeBytes / 2, p.k + a1, kCodeBytes / 2, &sh.kc_full);
+            }
+            ok = wait_for(sh, &sh.vc_empty, (n & 1) ^ 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) {   // the K codes on their way land before the CTA ends
+                tc::mbar_wait(&sh.kc_full, n & 1, clock64() + tc::kWaitCycles);
+                break;
+            }
+            if (lane == 0) {
+                tc::mbar_arrive_expect_tx(&sh.vc_full, bytes);
+                if (pg0 >= 0) tc::bulk_g2s(sVc, p.v + a0, kCodeBytes / 2, &sh.vc_full);
+                if (pg1 >= 0) tc::bulk_g2s(sVc + kCodeBytes / 2, p.v + a1, kCodeBytes / 2, &sh.vc_full);
+            }
+        }
+        if (ok) more = w.next(p);
+    }
+    // the copies of the last tile have landed before the CTA ends, whatever
+    // became of their readers
+    if (n > 0) {
+        tc::mbar_wait(&sh.kc_full, (n - 1) & 1, clock64() + tc::kWaitCycles);
+        tc::mbar_wait(&sh.vc_full, (n - 1) & 1, clock64() + tc::kWaitCycles);
+    }
+    if (!ok || !__all_sync(0xffffffffu, wait_for(sh, &sh.info_empty[n % kTiles], ((n / kTiles) & 1) ^ 1))) return;
+    if (lane == 0) {
+        sh.tile[n % kTiles].flags = kEnd;
+        tc::mbar_arrive(&sh.info_full[n % kTiles]);
+    }
+}
+
 template <int CODE, bool MOD>
 __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p) {
     extern __shared__ uint8_t dyn[];
@@ -200,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
     const int cta = blockIdx.x;
 
     // ---- this CTA's range -------------------------------------------------
-    // pairs of query tiles up to each request, then tiles up to each pair
+    // pairs of query tiles up to each request, then cost up to each pair
     int* s_pairs = reinterpret_cast<int*>(base);   // [batch + 1], before the tiles use it
     {
         const int chunk = (p.batch + kThreads - 1) / kThreads;
@@ -247,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
         const int first_b = b;
         for (int i = q0; i < q1; ++i) {
             while (i >= s_pairs[b + 1]) ++b;
-            mine += span_of(p, seen_of<kN>(p, b), i - s_pairs[b]).tiles;
+            mine += span_of(p, seen_of<kN>(p, b), i - s_pairs[b]).tiles + kPieceTiles;
         }
         int64_t incl = mine;
 #pragma unroll
@@ -276,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
                 b = first_b;
                 for (;; ++i) {
                     while (i >= s_pairs[b + 1]) ++b;
-                    const int n = span_of(p, seen_of<kN>(p, b), i - s_pairs[b]).tiles;
+                    const int n = span_of(p, seen_of<kN>(p, b), i - s_pairs[b]).tiles + kPieceTiles;
                     if (off < n) break;
                     off -= n;
                 }
@@ -291,21 +758,29 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
 
     // ---- barriers and tensor memory ---------------------------------------
     if (t == 0) {
+        for (int i = 0; i < kTiles; ++i) {
+            tc::mbar_init(&sh.info_full[i], 1);
+            tc::mbar_init(&sh.info_empty[i], kSoftmaxWarps + kCodeWarps + 1);
+        }
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&sh.k_full[i], 32 * kCodeWarps);
-            tc::mbar_init(&sh.v_full[i], 32 * kCodeWarps);
+            tc::mbar_init(&sh.k_full[i], kCodeWarps);
+            tc::mbar_init(&sh.v_full[i], kCodeWarps);
             tc::mbar_init(&sh.k_empty[i], 1);
             tc::mbar_init(&sh.v_empty[i], 1);
             tc::mbar_init(&sh.s_full[i], 1);
-            tc::mbar_init(&sh.p_full[i], kM);
+            tc::mbar_init(&sh.p_full[i], kSoftmaxWarps / 2);
             tc::mbar_init(&sh.pv_done[i], 1);
         }
-        tc::mbar_init(&sh.q_full, 2 * kM);
+        tc::mbar_init(&sh.kc_full, 1);
+        tc::mbar_init(&sh.vc_full, 1);
+        tc::mbar_init(&sh.kc_empty, kCodeWarps);
+        tc::mbar_init(&sh.vc_empty, kCodeWarps);
+        tc::mbar_init(&sh.q_full, kSoftmaxWarps);
         tc::mbar_init(&sh.drain, 1);
         sh.failed = 0;
         tc::fence_mbar_init();
     }
-    if (warp == kSoftmaxWarps + kCodeWarps) {
+    if (warp == kMmaWarp) {
         tc::tmem_alloc(&sh.tmem, 512);
         tc::tmem_relinquish();
     }
@@ -316,400 +791,28 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
     uint8_t* sK = base;
     uint8_t* sV = base + 2 * kTileBytes;
     uint8_t* sQ = base + 4 * kTileBytes;
-
-    Walk w;
-    w.start(p, start_h, sh.start_b, sh.start_pair, (int)sh.start_off, left);
+    uint8_t* sKc = base + 6 * kTileBytes;
+    uint8_t* sVc = sKc + kCodeBytes;
 
     if (warp < kSoftmaxWarps) {
-        // =================== softmax: one thread per row ====================
-        const int i = warp >> 2, row = t & (kM - 1);
-        const uint32_t quad = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + i * kN + quad, tO = tmem + 2 * kN + i * kHeadDim + quad;
-        uint8_t* q_row = sQ + i * kTileBytes + row * 128;
-        int n = 0;          // key tiles done
-        bool ok = true;
-        do {
-            // ---- this row's query ----
-            const int k = row / p.g;
-            const int token = w.pair * 2 * p.tq + i * p.tq + k;
-            const int head = w.h * p.g + row % p.g;
-            const bool on = k < p.tq && token < w.r.n;
-            float rowf;
-            {
-                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                                  (int64_t)(w.r.first + (on ? token : 0)) * p.q_stride +
-                                                                  head * kHeadDim);
-                uint4 x[16];
-                float top = 0.f;
-#pragma unroll
-                for (int c = 0; c < 16; ++c) x[c] = on ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xffff0000u))));
-                }
-                int up = 14 - ((int)(__float_as_uint(top) >> 23) - 127);
-                up = max(-126, min(126, up));
-                const float f = __uint_as_float((uint32_t)(up + 127) << 23);
-                rowf = __uint_as_float((uint32_t)(127 - up) << 23) * (p.scale * (MOD ? 1.f : kLog2e));
-#pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-                    uint32_t o[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const __half2 hh = __floats2half2_rn(__uint_as_float(v[e] << 16) * f,
-                                                             __uint_as_float(v[e] & 0xffff0000u) * f);
-                        o[e] = *reinterpret_cast<const uint32_t*>(&hh);
-                    }
-                    *reinterpret_cast<uint4*>(q_row + (c >> 3) * kHalf + (((c & 7) ^ (row & 7)) << 4)) =
-                        make_uint4(o[0], o[1], o[2], o[3]);
-                }
-            }
-            tc::fence_async_smem();
-            tc::mbar_arrive(&sh.q_full);
-
-            const int pos = w.r.len - w.r.n + min(token, w.r.n - 1);
-            const int see_from = p.window > 0 ? max(-1, pos - p.window) : -1;   // sees (see_from, pos] and the prefix
-            const float slope = MOD && p.slopes && on ? p.slopes[head] * kLog2e : 0.f;
-            // the span of positions of this warp's rows
-            const int wp_min = __reduce_min_sync(0xffffffffu, pos), wp_max = __reduce_max_sync(0xffffffffu, pos);
-            float M = -INFINITY, l = 0.f;
-
-            // page numbers two tiles ahead, scales one tile ahead
-            auto page_at = [&](int ti, int half) {
-                if (ti >= w.t1) return -1;
-                const int tok = w.span.tile_of(ti) * kN + half * kPage;
-                return tok < w.r.len ? __ldg(p.table + (int64_t)w.b * p.width + tok / kPage) : -1;
-            };
-            auto valid = [&](int page) { return page >= 0 && page < p.pages; };
-            int pg[2] = {page_at(w.t0, 0), page_at(w.t0, 1)};
-            float sk[2], sv[2];
-            bool there[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                there[e] = valid(pg[e]);
-                const int64_t at = (int64_t)(there[e] ? pg[e] : 0) * p.kv_heads + w.h;
-                sk[e] = there[e] ? __ldg(p.k_scale + at) : 0.f;
-                sv[e] = there[e] ? __ldg(p.v_scale + at) : 1.f;
-                pg[e] = page_at(w.t0 + 1, e);
-            }
-            for (int ti = w.t0; ti < w.t1; ++ti, ++n) {
-                float a[2], lsv[2], isv[2];
-                bool use[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    a[e] = rowf * sk[e];
-                    const float s = sv[e] > 0.f ? sv[e] : 1.f;
-                    lsv[e] = lg2(s);
-                    isv[e] = __fdividef(1.f, s);
-                    use[e] = there[e];
-                    there[e] = valid(pg[e]);
-                    const int64_t at = (int64_t)(there[e] ? pg[e] : 0) * p.kv_heads + w.h;
-                    sk[e] = there[e] ? __ldg(p.k_scale + at) : 0.f;
-                    sv[e] = there[e] ? __ldg(p.v_scale + at) : 1.f;
-                    pg[e] = page_at(ti + 2, e);
-                }
-                const int key0 = w.span.tile_of(ti) * kN;
-                const bool clear = use[0] && use[1] && key0 + kN <= w.r.len &&
-                                   ((key0 + kN - 1 <= wp_min && (p.window == 0 || key0 > wp_max - p.window)) ||
-                                    key0 + kN <= w.r.pre);
-                uint32_t mask[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-                if (!clear) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int k0 = key0 + 32 * c;
-                        mask[c] = (bits(see_from + 1 - k0, pos + 1 - k0) | bits(0, w.r.pre - k0)) & bits(0, w.r.len - k0);
-                        if (!use[c >> 1]) mask[c] = 0u;
-                    }
-                }
-                ok = ok && wait_for(sh, &sh.s_full[i], n & 1);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc::tc_fence_after();
-
-                // ---- the row's maximum ----
-                float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t s[32];
-                    tmem_ld32(tS + 32 * c, s);
-                    tc::tmem_wait_ld();
-                    if (MOD) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            float x = __uint_as_float(s[e]) * a[c >> 1];
-                            if (p.cap > 0.f) x = p.cap * tanh_abs(__fdividef(x, p.cap));
-                            x = x * kLog2e - slope * fabsf((float)(pos - (key0 + 32 * c + e)));
-                            s[e] = __float_as_uint(x);
-                        }
-                        tmem_st32(tS + 32 * c, s);
-                    }
-                    float m = -INFINITY;
-                    if (clear) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) m = fmaxf(m, __uint_as_float(s[e]));
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) m = fmaxf(m, (mask[c] >> e) & 1u ? __uint_as_float(s[e]) : -INFINITY);
-                    }
-                    top[c >> 1] = fmaxf(top[c >> 1], m);
-                }
-                if (MOD) {
-                    tc::tmem_wait_st();
-                    a[0] = a[1] = 1.f;
-                }
-                float now = -INFINITY;
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (top[e] > -INFINITY) now = fmaxf(now, fmaf(top[e], a[e], lsv[e]));
-                const bool raise = now > M + kRaise || (M == -INFINITY && now > -INFINITY);
-                if (__any_sync(0xffffffffu, raise)) {
-                    const float f = raise && M > -INFINITY ? ex2(M - now) : 1.f;
-                    if (raise) M = now;
-                    l *= f;
-                    if (ti > w.t0) {   // the accumulator holds earlier tiles
-                        ok = wait_for(sh, &sh.pv_done[i], (n - 1) & 1);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
-                        tc::tc_fence_after();
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t o[32];
-                            tmem_ld32(tO + 32 * c, o);
-                            tc::tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st32(tO + 32 * c, o);
-                        }
-                    }
-                }
-                // ---- weights ----
-                // One fused multiply-add per weight: x - M with x unrounded, M and
-                // M - log2 s_v rounded, off by 2^-24 |M| between pages.  Beyond
-                // |M| = 2^10 (and for hidden keys) x is rounded like M was, so that
-                // the row's largest key gives exactly x - M = 0.
-                const float Mb = M == -INFINITY ? 0.f : M;
-                const bool plain = clear && __all_sync(0xffffffffu, fabsf(Mb) < 1024.f);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t s[32], o[16];
-                    tmem_ld32(tS + 32 * c, s);
-                    tc::tmem_wait_ld();
-                    const float aa = a[c >> 1], ls = lsv[c >> 1], bb = ls + (kShift - Mb);
-                    float sum = 0.f;
-                    if (plain) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float x = ex2(fmaf(__uint_as_float(s[e]), aa, bb));
-                            const float y = ex2(fmaf(__uint_as_float(s[e + 1]), aa, bb));
-                            sum += x + y;
-                            const __half2 hh = __floats2half2_rn(x, y);
-                            o[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float x = ex2((fmaf(__uint_as_float(s[e]), aa, ls) - Mb) + kShift);
-                            float y = ex2((fmaf(__uint_as_float(s[e + 1]), aa, ls) - Mb) + kShift);
-                            x = (mask[c] >> e) & 1u ? x : 0.f;
-                            y = (mask[c] >> (e + 1)) & 1u ? y : 0.f;
-                            sum += x + y;
-                            const __half2 hh = __floats2half2_rn(x, y);
-                            o[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
-                        }
-                    }
-                    l += sum * isv[c >> 1];
-                    tc::tmem_st16(tS + 16 * c, o);
-                }
-                tc::tmem_wait_st();
-                tc::tc_fence_before();
-                tc::mbar_arrive(&sh.p_full[i]);
-            }
-            if (!ok) break;
-
-            // ---- end of the piece ----
-            ok = wait_for(sh, &sh.pv_done[i], (n - 1) & 1);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc::tc_fence_after();
-            const bool whole = w.whole();
-            const int slot = cta * 2 + (w.t0 == 0 ? 1 : 0);
-            const int64_t at = (int64_t)slot * (2 * kM) + i * kM + row;
-            const float inv = l > 0.f ? __fdiv_rn(1.f, l) : (l == 0.f ? 0.f : l);
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
-                                 ((int64_t)(w.r.first + token) * p.kv_heads * p.g + head) * kHeadDim;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t o[32];
-                __syncwarp();
-                tmem_ld32(tO + 32 * c, o);
-                tc::tmem_wait_ld();
-                if (!on) {
-                } else if (whole) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint32_t v[4];
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) {
-                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * z]) * inv,
-                                                                            __uint_as_float(o[e + 2 * z + 1]) * inv);
-                            v[z] = *reinterpret_cast<const uint32_t*>(&b2);
-                        }
-                        *reinterpret_cast<uint4*>(out + 32 * c + e) = make_uint4(v[0], v[1], v[2], v[3]);
-                    }
-                } else {
-                    float4* to = reinterpret_cast<float4*>(p.part + at * kHeadDim + 32 * c);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        to[e / 4] = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                                                __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-                }
-            }
-            if (!whole) {
-                if (on) *reinterpret_cast<float2*>(p.ml + at * 2) = make_float2(M, l);
-                if (t == 0) {
-                    int* m = p.meta + cta * kMeta;
-                    if (w.t0 > 0) {
-                        m[0] = w.t1 == w.span.tiles;
-                    } else {
-                        m[1] = 1;
-                        m[2] = w.b;
-                        m[3] = w.h;
-                        m[4] = w.pair;
-                    }
-                }
-            }
-            tc::tc_fence_before();
-        } while (w.next(p));
+        more_registers<kSoftmaxRegs>();
+        softmax_role<MOD>(p, sh, sQ, tmem, warp, lane);
     } else if (warp < kSoftmaxWarps + kCodeWarps) {
-        // =================== codes to operand tiles =========================
-        // Per pass a warp takes 4 rows of 128 codes, 8 lanes a row.  A lane's 16
-        // codes become chunks 2c and 2c + 1 of one 64-column half; lanes of the
-        // second half store theirs in the other order, which keeps the 8 lanes
-        // of a row on different banks.
-        const int u = t - 32 * kSoftmaxWarps;
-        const int c = u & 7, row0 = u >> 3;           // 16 rows per pass, 8 passes
-        const int first = c >> 2;                     // which of its two chunks goes first
-        int n = 0;
-        uint4 ck[8], cv[8];
-        auto load = [&](int ti) {
-            const int tok0 = w.span.tile_of(ti) * kN;
-            int pages[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int tok = tok0 + e * kPage;
-                pages[e] = tok < w.r.len ? __ldg(p.table + (int64_t)w.b * p.width + tok / kPage) : -1;
-            }
-#pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                const int rr = s * 16 + row0;
-                const int page = pages[s >> 2];
-                const bool on = page >= 0 && page < p.pages && tok0 + rr < w.r.len;
-                const int64_t at = ((int64_t)page * p.kv_heads + w.h) * (kPage * kHeadDim) + (rr & (kPage - 1)) * kHeadDim + c * 16;
-                ck[s] = on ? __ldg(reinterpret_cast<const uint4*>(p.k + at)) : make_uint4(0u, 0u, 0u, 0u);
-                cv[s] = on ? __ldg(reinterpret_cast<const uint4*>(p.v + at)) : make_uint4(0u, 0u, 0u, 0u);
-            }
-        };
-        auto put = [&](uint8_t* tile, const uint4 (&x)[8]) {
-#pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                const int rr = s * 16 + row0;
-                uint8_t* to = tile + (c >> 2) * kHalf + rr * 128;
-                const uint32_t v[4] = {Codes<CODE>::bias(x[s].x), Codes<CODE>::bias(x[s].y), Codes<CODE>::bias(x[s].z),
-                                       Codes<CODE>::bias(x[s].w)};
-                const uint4 lo = make_uint4(Codes<CODE>::lo(v[0]), Codes<CODE>::hi(v[0]), Codes<CODE>::lo(v[1]), Codes<CODE>::hi(v[1]));
-                const uint4 hi = make_uint4(Codes<CODE>::lo(v[2]), Codes<CODE>::hi(v[2]), Codes<CODE>::lo(v[3]), Codes<CODE>::hi(v[3]));
-                const int c0 = 2 * (c & 3);
-                *reinterpret_cast<uint4*>(to + (((c0 + first) ^ (rr & 7)) << 4)) = first ? hi : lo;
-                *reinterpret_cast<uint4*>(to + (((c0 + 1 - first) ^ (rr & 7)) << 4)) = first ? lo : hi;
-            }
-        };
-        bool ok = true;
-        load(w.t0);
-        int ti = w.t0;
-        for (;;) {
-            const int st = n & 1;
-            const uint32_t free_par = ((n >> 1) & 1) ^ 1;
-            ok = wait_for(sh, &sh.k_empty[st], free_par);
-            if (!ok) break;
-            put(sK + st * kTileBytes, ck);
-            tc::fence_async_smem();
-            tc::mbar_arrive(&sh.k_full[st]);
-            ok = wait_for(sh, &sh.v_empty[st], free_par);
-            if (!ok) break;
-            put(sV + st * kTileBytes, cv);
-            tc::fence_async_smem();
-            tc::mbar_arrive(&sh.v_full[st]);
-            ++n;
-            if (++ti == w.t1) {
-                if (!w.next(p)) break;
-                ti = w.t0;
-            }
-            load(ti);
+        fewer_registers<kCodeRegs>();
+        code_role<CODE>(sh, sK, sV, sKc, sVc, t - 32 * kSoftmaxWarps, lane);
+    } else {
+        fewer_registers<kOtherRegs>();
+        if (warp == kMmaWarp) {
+            if (lane == 0) mma_role(sh, sK, sV, sQ, tmem);
+        } else if (warp == kWalkWarp) {
+            walk_role(p, sh, sKc, sVc, start_h, left, lane);
         }
-    } else if (lane == 0) {
-        // =================== MMA ============================================
-        const uint32_t idS = tc::idesc_f32acc(0, kM, kN, 0, 0), idO = tc::idesc_f32acc(0, kM, kHeadDim, 0, 1);
-        const uint32_t aK = tc::smem_u32(sK), aV = tc::smem_u32(sV), aQ = tc::smem_u32(sQ);
-        auto scores = [&](int i, int st) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t o = (k >> 2) * kHalf + (k & 3) * 32;
-                tc::mma_f16_ss(tmem + i * kN, desc_sw128(aQ + i * kTileBytes + o, 16, 1024),
-                               desc_sw128(aK + st * kTileBytes + o, 16, 1024), idS, k > 0);
-            }
-            tc::mma_commit(&sh.s_full[i]);
-        };
-        auto values = [&](int i, int st, bool more) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                tc::mma_f16_ts(tmem + 2 * kN + i * kHeadDim, tmem + i * kN + k * 8,
-                               desc_sw128(aV + st * kTileBytes + k * 2048, kHalf, 1024), idO, more || k > 0);
-            tc::mma_commit(&sh.pv_done[i]);
-        };
-        int n = 0, piece = 0;
-        bool ok = true;
-        do {
-            ok = wait_for(sh, &sh.q_full, piece & 1) && wait_for(sh, &sh.k_full[n & 1], (n >> 1) & 1);
-            if (!ok) break;
-            tc::tc_fence_after();
-            scores(0, n & 1);
-            scores(1, n & 1);
-            tc::mma_commit(&sh.k_empty[n & 1]);
-            for (int ti = w.t0; ti < w.t1 && ok; ++ti, ++n) {
-                const bool more = ti + 1 < w.t1;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (i == 0) ok = wait_for(sh, &sh.v_full[n & 1], (n >> 1) & 1);
-                    ok = ok && wait_for(sh, &sh.p_full[i], n & 1);
-                    if (!ok) break;
-                    tc::tc_fence_after();
-                    values(i, n & 1, ti > w.t0);
-                    if (i == 1) tc::mma_commit(&sh.v_empty[n & 1]);
-                    if (more) {
-                        if (i == 0) ok = wait_for(sh, &sh.k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
-                        if (!ok) break;
-                        tc::tc_fence_after();
-                        scores(i, (n + 1) & 1);
-                        if (i == 1) tc::mma_commit(&sh.k_empty[(n + 1) & 1]);
-                    }
-                }
-            }
-            ++piece;
-        } while (ok && w.next(p));
-        // every MMA has ended before tensor memory is given back
-        tc::mma_commit(&sh.drain);
-        const long long deadline = clock64() + tc::kWaitCycles;
-        tc::mbar_wait(&sh.drain, 0, deadline);
     }
     __syncwarp();
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    if (warp == kSoftmaxWarps + kCodeWarps) tc::tmem_dealloc(tmem, 512);
+    if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
     if (t == 0 && sh.failed && p.status) atomicMin(p.status, ISKV_ERR_DEVICE_TIMEOUT);
 }
 
