@@ -69,8 +69,8 @@ constexpr int kTiles = 4;
 struct Shared {
     Tile tile[kTiles];
     uint64_t info_full[kTiles], info_empty[kTiles];
-    uint64_t kc_full, kc_empty, vc_full, vc_empty;
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+    uint64_t c_full[2], c_empty[2];           // codes of K, of V
+    uint64_t full[2][2], empty[2][2];         // operand tiles of K, of V: two buffers each
     uint64_t q_full, s_full[2], p_full[2], pv_done[2], drain;
     uint32_t tmem;
     int failed;
@@ -102,6 +102,33 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
           "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(taddr));
 }
+// Two fp32 operations per instruction.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint32_t x, uint32_t y, uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tfma.rn.f32x2 %0, t, %3, %4;\n\t}" : "=l"(r) : "r"(x), "r"(y), "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float2 split(uint64_t a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // Shared-memory operand with 128-byte rows, 128-byte swizzle (the 16-byte chunk
 // c of row t stands at chunk c ^ (t & 7)).  K-major (Q, K): sbo = 1024 between
 // groups of 8 rows.  MN-major (V, whose rows are the reduction index): sbo =
@@ -112,8 +139,7 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uin
 }
 
 // Waits are bounded: the limit is about a second, a pipeline step microseconds.
-__device__ __forceinline__ bool wait_for(Shared& sh, uint64_t* bar, uint32_t parity) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
+__device__ __forceinline__ bool wait_longer(Shared& sh, uint64_t* bar, uint32_t parity) {
     const long long deadline = clock64() + tc::kWaitCycles;
     while (!tc::mbar_try_wait(bar, parity)) {
         if (*(volatile int*)&sh.failed) return false;
@@ -123,6 +149,9 @@ __device__ __forceinline__ bool wait_for(Shared& sh, uint64_t* bar, uint32_t par
         }
     }
     return true;
+}
+__device__ __forceinline__ bool wait_for(Shared& sh, uint64_t* bar, uint32_t parity) {
+    return tc::mbar_try_wait(bar, parity) || wait_longer(sh, bar, parity);
 }
 
 // The key tiles that a pair of query tiles sees.
@@ -233,41 +262,50 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
         ok = __all_sync(0xffffffffu, ok);
         if (!ok || (flags & kEnd)) return;
 
-        if (flags & kFirst) {   // this row's query
+        if (flags & kFirst) {   // the warp's 32 queries, two rows per load, 16 lanes a row
             token = ti.token0 + i * p.tq + k;
             head = ti.h * p.g + hg;
             on = k < p.tq && token < ti.n;
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                              (int64_t)(ti.first + (on ? token : 0)) * p.q_stride +
-                                                              head * kHeadDim);
-            uint4 x[16];
-            float top = 0.f;
+            // (rolled: straight-line code that runs once per piece costs more in
+            // instruction fetches than it saves)
+            const int c = lane & 15;
+            const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)ti.first * p.q_stride + c * 8;
+            int64_t at = on ? (int64_t)token * p.q_stride + head * kHeadDim : -1;   // of this thread's row
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+                uint4 x[8];
 #pragma unroll
-            for (int c = 0; c < 16; ++c) x[c] = on ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xffff0000u))));
-            }
-            int up = 14 - ((int)(__float_as_uint(top) >> 23) - 127);
-            up = max(-126, min(126, up));
-            const float f = __uint_as_float((uint32_t)(up + 127) << 23);
-            rowf = __uint_as_float((uint32_t)(127 - up) << 23) * (p.scale * (MOD ? 1.f : kLog2e));
-            uint8_t* q_row = sQ + i * kTileBytes + row * 128;
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-                uint32_t o[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const __half2 hh = __floats2half2_rn(__uint_as_float(v[e] << 16) * f,
-                                                         __uint_as_float(v[e] & 0xffff0000u) * f);
-                    o[e] = *reinterpret_cast<const uint32_t*>(&hh);
+                for (int z = 0; z < 8; ++z) {
+                    const int64_t src = __shfl_sync(0xffffffffu, at, b * 16 + 2 * z + (lane >> 4));
+                    x[z] = src >= 0 ? __ldg(reinterpret_cast<const uint4*>(q0 + src)) : make_uint4(0u, 0u, 0u, 0u);
                 }
-                *reinterpret_cast<uint4*>(q_row + (c >> 3) * kHalf + (((c & 7) ^ (row & 7)) << 4)) =
-                    make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+                for (int z = 0; z < 8; ++z) {
+                    const int r32 = b * 16 + 2 * z + (lane >> 4);
+                    const uint32_t v[4] = {x[z].x, x[z].y, x[z].z, x[z].w};
+                    // bf16 magnitudes order like their bits: the row's largest exponent
+                    uint32_t top = __vmaxu2(__vmaxu2(v[0] & 0x7fff7fffu, v[1] & 0x7fff7fffu),
+                                            __vmaxu2(v[2] & 0x7fff7fffu, v[3] & 0x7fff7fffu));
+                    top = max(top >> 16, top & 0xffffu);
+                    const uint32_t half = lane < 16 ? 0x0000ffffu : 0xffff0000u;
+                    top = __reduce_max_sync(half, top);
+                    // 2^up brings the row's largest element into [2^14, 2^15)
+                    const int up = max(-126, min(126, 14 - ((int)(top >> 7) - 127)));
+                    const float f = __uint_as_float((uint32_t)(up + 127) << 23);
+                    uint32_t o[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const __half2 hh = __floats2half2_rn(__uint_as_float(v[e] << 16) * f,
+                                                             __uint_as_float(v[e] & 0xffff0000u) * f);
+                        o[e] = *reinterpret_cast<const uint32_t*>(&hh);
+                    }
+                    *reinterpret_cast<uint4*>(sQ + i * kTileBytes + (c >> 3) * kHalf + ((warp & 3) * 32 + r32) * 128 +
+                                              (((c & 7) ^ (r32 & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    // the row's own thread keeps 2^-up
+                    const int mine = __shfl_sync(0xffffffffu, up, (lane & 1) << 4);
+                    if ((lane & ~1) == b * 16 + 2 * z)
+                        rowf = __uint_as_float((uint32_t)(127 - mine) << 23) * (p.scale * (MOD ? 1.f : kLog2e));
+                }
             }
             tc::fence_async_smem();
             __syncwarp();
@@ -325,7 +363,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
             for (int e = 0; e < kN; e += 2) {
                 const int z = (e >> 1) & 3;
                 float& r = m[e < kPage ? z : 4 + z];
-                r = fmaxf(r, fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
+                r = max3(r, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
             }
             t0 = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
             t1 = fmaxf(fmaxf(m[4], m[5]), fmaxf(m[6], m[7]));
@@ -354,44 +392,36 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
         }
         // ---- weights ----
         // One fused multiply-add per weight: x - M with x unrounded, M and
-        // M - log2 s_v rounded, off by 2^-24 |M| between pages.  Beyond
-        // |M| = 2^10 x is rounded like M was, so that the row's largest key
-        // gives exactly x - M = 0.
+        // M - log2 s_v rounded, off by 2^-24 |M| between pages.  From
+        // |M| = 2^10 on, x is rounded like M was first, so that the row's
+        // largest key gives exactly x - M = 0.
         const float Mb = M == -INFINITY ? 0.f : M;
-        float sum0 = 0.f, sum1 = 0.f;
-        if (__all_sync(0xffffffffu, fabsf(Mb) < 1024.f)) {
-            const float b0 = lsv0 + (kShift - Mb), b1 = lsv1 + (kShift - Mb);
+        float b0 = lsv0 + (kShift - Mb), b1 = lsv1 + (kShift - Mb);
+        if (__any_sync(0xffffffffu, fabsf(Mb) >= 1024.f)) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t o[16];
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float x = ex2(fmaf(__uint_as_float(s[32 * c + e]), c < 2 ? a0 : a1, c < 2 ? b0 : b1));
-                    const float y = ex2(fmaf(__uint_as_float(s[32 * c + e + 1]), c < 2 ? a0 : a1, c < 2 ? b0 : b1));
-                    if (c < 2) sum0 += x + y;
-                    else sum1 += x + y;
-                    const __half2 hh = __floats2half2_rn(x, y);
-                    o[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
-                }
-                tc::tmem_st16(tS + 16 * c, o);
-            }
-        } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t o[16];
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float x = ex2((fmaf(__uint_as_float(s[32 * c + e]), c < 2 ? a0 : a1, c < 2 ? lsv0 : lsv1) - Mb) + kShift);
-                    const float y = ex2((fmaf(__uint_as_float(s[32 * c + e + 1]), c < 2 ? a0 : a1, c < 2 ? lsv0 : lsv1) - Mb) + kShift);
-                    if (c < 2) sum0 += x + y;
-                    else sum1 += x + y;
-                    const __half2 hh = __floats2half2_rn(x, y);
-                    o[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
-                }
-                tc::tmem_st16(tS + 16 * c, o);
-            }
+            for (int e = 0; e < kN; ++e)
+                s[e] = __float_as_uint(fmaf(__uint_as_float(s[e]), e < kPage ? a0 : a1, e < kPage ? lsv0 : lsv1) - Mb);
+            a0 = a1 = 1.f;
+            b0 = b1 = kShift;
         }
-        l += sum0 * ti.isv[0] + sum1 * ti.isv[1];
+        const uint64_t aa[2] = {pair(a0, a0), pair(a1, a1)}, bb[2] = {pair(b0, b0), pair(b1, b1)};
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint32_t o[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+                float2 x = split(fma2(s[32 * c + e], s[32 * c + e + 1], aa[c >> 1], bb[c >> 1]));
+                x.x = ex2(x.x);
+                x.y = ex2(x.y);
+                sum[c >> 1] = add2(sum[c >> 1], pair(x.x, x.y));
+                const __half2 hh = __floats2half2_rn(x.x, x.y);
+                o[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
+            }
+            tc::tmem_st16(tS + 16 * c, o);
+        }
+        const float2 s0 = split(sum[0]), s1 = split(sum[1]);
+        l += (s0.x + s0.y) * ti.isv[0] + (s1.x + s1.y) * ti.isv[1];
         tc::tmem_wait_st();
         tc::tc_fence_before();
         __syncwarp();
@@ -404,33 +434,56 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
             const int slot = ti.slot;
             const int64_t at = (int64_t)slot * (2 * kM) + i * kM + row;
             const float inv = l > 0.f ? __fdiv_rn(1.f, l) : (l == 0.f ? 0.f : l);
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
-                                 ((int64_t)(ti.first + token) * p.kv_heads * p.g + head) * kHeadDim;
+            // through the warp's own Q rows (their products are done), so that whole
+            // rows are written: a row's thread puts 64 bytes at a time in its row's
+            // two halves, then 16 lanes write a row of bf16, 32 lanes one of fp32
+            uint8_t* const mine = sQ + i * kTileBytes + (warp & 3) * 32 * 128;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t o[32];
+            for (int part = 0; part < 2; ++part) {   // 64 of the 128 columns
+                uint32_t o[64];
                 __syncwarp();
-                tmem_ld32(tO + 32 * c, o);
+                tmem_ld32(tO + 64 * part, *reinterpret_cast<uint32_t(*)[32]>(o));
+                tmem_ld32(tO + 64 * part + 32, *reinterpret_cast<uint32_t(*)[32]>(o + 32));
                 tc::tmem_wait_ld();
-                if (!on) {
-                } else if (slot < 0) {
+                if (slot < 0) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
+                    for (int c = 0; c < 8; ++c) {
                         uint32_t v[4];
 #pragma unroll
                         for (int z = 0; z < 4; ++z) {
-                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * z]) * inv,
-                                                                            __uint_as_float(o[e + 2 * z + 1]) * inv);
+                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * c + 2 * z]) * inv,
+                                                                            __uint_as_float(o[8 * c + 2 * z + 1]) * inv);
                             v[z] = *reinterpret_cast<const uint32_t*>(&b2);
                         }
-                        *reinterpret_cast<uint4*>(out + 32 * c + e) = make_uint4(v[0], v[1], v[2], v[3]);
+                        *reinterpret_cast<uint4*>(mine + part * kHalf + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                            make_uint4(v[0], v[1], v[2], v[3]);
                     }
-                } else {
-                    float4* to = reinterpret_cast<float4*>(p.part + at * kHeadDim + 32 * c);
+                    if (part == 0) continue;
+                    __syncwarp();
+                    const int c = lane & 15;
+                    __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(p.out) + c * 8;
+                    const int64_t own = on ? ((int64_t)(ti.first + token) * p.kv_heads * p.g + head) * kHeadDim : -1;
+#pragma unroll 2
+                    for (int z = 0; z < 16; ++z) {
+                        const int r32 = 2 * z + (lane >> 4);
+                        const uint4 v = *reinterpret_cast<const uint4*>(mine + (c >> 3) * kHalf + r32 * 128 + (((c & 7) ^ (r32 & 7)) << 4));
+                        const int64_t to = __shfl_sync(0xffffffffu, own, r32);
+                        if (to >= 0) *reinterpret_cast<uint4*>(out + to) = v;
+                    }
+                } else {   // fp32: 64 columns are 256 bytes, 128 in each half
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        to[e / 4] = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                                                __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+                    for (int c = 0; c < 16; ++c)
+                        *reinterpret_cast<uint4*>(mine + (c >> 3) * kHalf + lane * 128 + (((c & 7) ^ (lane & 7)) << 4)) =
+                            make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                    __syncwarp();
+                    const int c = lane & 15;
+#pragma unroll 2
+                    for (int z = 0; z < 16; ++z) {
+                        const int r32 = 2 * z + (lane >> 4);
+                        const uint4 v = *reinterpret_cast<const uint4*>(mine + (c >> 3) * kHalf + r32 * 128 + (((c & 7) ^ (r32 & 7)) << 4));
+                        *reinterpret_cast<uint4*>(p.part + ((int64_t)slot * (2 * kM) + i * kM + (warp & 3) * 32 + r32) * kHeadDim +
+                                                  64 * part + 4 * c) = v;
+                    }
                 }
             }
             if (slot >= 0 && on) *reinterpret_cast<float2*>(p.ml + at * 2) = make_float2(M, l);
@@ -442,35 +495,37 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
 }
 
 // =================== codes to operand tiles =================================
-// Per pass 8 threads take a row of 128 codes.  A thread's 16 codes become
-// chunks 2c and 2c + 1 of one 64-column half; threads of the second half store
-// theirs in the other order, which keeps the 8 threads of a row on different
-// banks.
+// Per pass 8 threads take 128 codes, 16 each, which become two neighbouring
+// 16-byte chunks of one 64-column half.  The 4 threads of the second half take
+// the neighbouring row: its swizzle differs in the lowest bit, so the 8 stores
+// go to different banks.
 template <int CODE>
 __device__ __forceinline__ void code_tile(uint8_t* tile, const uint8_t* codes, int u, int rows0, int rows1) {
-    const int c = u & 7, row0 = u >> 3, first = c >> 2, c0 = 2 * (c & 3);
+    const int c = u & 7, row0 = (u >> 3) ^ (c >> 2), c0 = 2 * (c & 3);
     uint4 x[8];
 #pragma unroll
-    for (int s = 0; s < 8; ++s) {
-        const int rr = s * 16 + row0;
-        x[s] = *reinterpret_cast<const uint4*>(codes + rr * kHeadDim + c * 16);
-        if ((rr & (kPage - 1)) >= (s < 4 ? rows0 : rows1)) x[s] = make_uint4(0u, 0u, 0u, 0u);   // behind the last token
+    for (int s = 0; s < 8; ++s) x[s] = *reinterpret_cast<const uint4*>(codes + (s * 16 + row0) * kHeadDim + c * 16);
+    if (rows0 < kPage || rows1 < kPage) {   // behind the last token, or a page that is not there
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            if (((s * 16 + row0) & (kPage - 1)) >= (s < 4 ? rows0 : rows1)) x[s] = make_uint4(0u, 0u, 0u, 0u);
     }
+    uint8_t* const to = tile + (c >> 2) * kHalf + row0 * 128;
+    uint8_t* const to0 = to + ((c0 ^ (row0 & 7)) << 4);
+    uint8_t* const to1 = to + (((c0 + 1) ^ (row0 & 7)) << 4);
 #pragma unroll
     for (int s = 0; s < 8; ++s) {
-        const int rr = s * 16 + row0;
-        uint8_t* to = tile + (c >> 2) * kHalf + rr * 128;
         const uint32_t v[4] = {Codes<CODE>::bias(x[s].x), Codes<CODE>::bias(x[s].y), Codes<CODE>::bias(x[s].z),
                                Codes<CODE>::bias(x[s].w)};
-        const uint4 lo = make_uint4(Codes<CODE>::lo(v[0]), Codes<CODE>::hi(v[0]), Codes<CODE>::lo(v[1]), Codes<CODE>::hi(v[1]));
-        const uint4 hi = make_uint4(Codes<CODE>::lo(v[2]), Codes<CODE>::hi(v[2]), Codes<CODE>::lo(v[3]), Codes<CODE>::hi(v[3]));
-        *reinterpret_cast<uint4*>(to + (((c0 + first) ^ (rr & 7)) << 4)) = first ? hi : lo;
-        *reinterpret_cast<uint4*>(to + (((c0 + 1 - first) ^ (rr & 7)) << 4)) = first ? lo : hi;
+        *reinterpret_cast<uint4*>(to0 + s * 2048) =
+            make_uint4(Codes<CODE>::lo(v[0]), Codes<CODE>::hi(v[0]), Codes<CODE>::lo(v[1]), Codes<CODE>::hi(v[1]));
+        *reinterpret_cast<uint4*>(to1 + s * 2048) =
+            make_uint4(Codes<CODE>::lo(v[2]), Codes<CODE>::hi(v[2]), Codes<CODE>::lo(v[3]), Codes<CODE>::hi(v[3]));
     }
 }
 
 template <int CODE>
-__device__ __forceinline__ void code_role(Shared& sh, uint8_t* sK, uint8_t* sV, const uint8_t* sKc, const uint8_t* sVc, int u, int lane) {
+__device__ __forceinline__ void code_role(Shared& sh, uint8_t* sK, const uint8_t* sKc, int u, int lane) {
     for (int n = 0;; ++n) {
         const Tile& ti = sh.tile[n % kTiles];
         if (!wait_for(sh, &sh.info_full[n % kTiles], (n / kTiles) & 1) || (ti.flags & kEnd)) return;
@@ -478,23 +533,18 @@ __device__ __forceinline__ void code_role(Shared& sh, uint8_t* sK, uint8_t* sV, 
         const int rows0 = ti.there[0] ? min(kPage, rows) : 0, rows1 = ti.there[1] ? min(kPage, rows - kPage) : 0;
         const int st = n & 1;
         const uint32_t par = (n >> 1) & 1;
-        if (!wait_for(sh, &sh.kc_full, n & 1) || !wait_for(sh, &sh.k_empty[st], par ^ 1)) return;
-        code_tile<CODE>(sK + st * kTileBytes, sKc, u, rows0, rows1);
-        tc::fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            tc::mbar_arrive(&sh.k_full[st]);
-            tc::mbar_arrive(&sh.kc_empty);
+#pragma unroll 1
+        for (int v = 0; v < 2; ++v) {   // K, then V
+            if (!wait_for(sh, &sh.c_full[v], n & 1) || !wait_for(sh, &sh.empty[v][st], par ^ 1)) return;
+            code_tile<CODE>(sK + (2 * v + st) * kTileBytes, sKc + v * kCodeBytes, u, rows0, rows1);
+            tc::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tc::mbar_arrive(&sh.full[v][st]);
+                tc::mbar_arrive(&sh.c_empty[v]);
+            }
         }
-        if (!wait_for(sh, &sh.vc_full, n & 1) || !wait_for(sh, &sh.v_empty[st], par ^ 1)) return;
-        code_tile<CODE>(sV + st * kTileBytes, sVc, u, rows0, rows1);
-        tc::fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            tc::mbar_arrive(&sh.v_full[st]);
-            tc::mbar_arrive(&sh.vc_empty);
-            tc::mbar_arrive(&sh.info_empty[n % kTiles]);
-        }
+        if (lane == 0) tc::mbar_arrive(&sh.info_empty[n % kTiles]);
     }
 }
 
@@ -527,30 +577,31 @@ __device__ __forceinline__ void mma_role(Shared& sh, const uint8_t* sK, const ui
         if (flags & kEnd) break;
         const int st = n & 1;
         if (flags & kFirst) {
-            if (!wait_for(sh, &sh.q_full, piece & 1) || !wait_for(sh, &sh.k_full[st], (n >> 1) & 1)) break;
+            if (!wait_for(sh, &sh.q_full, piece & 1) || !wait_for(sh, &sh.full[0][st], (n >> 1) & 1)) break;
             ++piece;
             tc::tc_fence_after();
-            scores(0, st);
-            scores(1, st);
-            tc::mma_commit(&sh.k_empty[st]);
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) scores(i, st);
+            tc::mma_commit(&sh.empty[0][st]);
         }
         const int nx = n + 1, sx = nx & 1;
-        if (!wait_for(sh, &sh.v_full[st], (n >> 1) & 1) || !wait_for(sh, &sh.p_full[0], n & 1)) break;
-        tc::tc_fence_after();
-        values(0, st, !(flags & kFirst));
-        if (!(flags & kLast)) {
-            if (!wait_for(sh, &sh.k_full[sx], (nx >> 1) & 1)) break;
+        bool ok = true;
+#pragma unroll 1
+        for (int i = 0; i < 2 && ok; ++i) {
+            ok = (i == 1 || wait_for(sh, &sh.full[1][st], (n >> 1) & 1)) && wait_for(sh, &sh.p_full[i], n & 1);
+            if (!ok) break;
             tc::tc_fence_after();
-            scores(0, sx);
+            values(i, st, !(flags & kFirst));
+            if (i == 1) tc::mma_commit(&sh.empty[1][st]);
+            if (!(flags & kLast)) {
+                ok = i == 1 || wait_for(sh, &sh.full[0][sx], (nx >> 1) & 1);
+                if (!ok) break;
+                tc::tc_fence_after();
+                scores(i, sx);
+                if (i == 1) tc::mma_commit(&sh.empty[0][sx]);
+            }
         }
-        if (!wait_for(sh, &sh.p_full[1], n & 1)) break;
-        tc::tc_fence_after();
-        values(1, st, !(flags & kFirst));
-        tc::mma_commit(&sh.v_empty[st]);
-        if (!(flags & kLast)) {
-            scores(1, sx);
-            tc::mma_commit(&sh.k_empty[sx]);
-        }
+        if (!ok) break;
         tc::mbar_arrive(&sh.info_empty[n % kTiles]);
     }
     // every MMA has ended before tensor memory is given back
@@ -559,7 +610,7 @@ __device__ __forceinline__ void mma_role(Shared& sh, const uint8_t* sK, const ui
 }
 
 // =================== the walk ===============================================
-__device__ __forceinline__ void walk_role(const AttnArgs& p, Shared& sh, uint8_t* sKc, uint8_t* sVc, int start_h, int64_t left, int lane) {
+__device__ __forceinline__ void walk_role(const AttnArgs& p, Shared& sh, uint8_t* sKc, int start_h, int64_t left, int lane) {
     Walk w;
     bool more = w.start(p, start_h, sh.start_b, sh.start_pair, sh.start_off, left);
     if (!more) more = w.next(p);
@@ -577,6 +628,16 @@ __device__ __forceinline__ void walk_role(const AttnArgs& p, Shared& sh, uint8_t
                 m[2] = w.b;
                 m[3] = w.h;
                 m[4] = w.pair;
+            }
+        }
+        // its queries are on their way to L2 while the piece before is worked on
+        for (int row = lane; row < 2 * kM; row += 32) {
+            const int rr = row & (kM - 1), k = rr / p.g, token = w.pair * 2 * p.tq + (row / kM) * p.tq + k;
+            if (k < p.tq && token < w.r.n) {
+                const __nv_bfloat16* at = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)(w.r.first + token) * p.q_stride +
+                                          (w.h * p.g + rr % p.g) * kHeadDim;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 64));
             }
         }
         int page = -1;
@@ -623,33 +684,30 @@ __device__ __forceinline__ void walk_role(const AttnArgs& p, Shared& sh, uint8_t
             const uint32_t bytes = (pg0 >= 0 ? kCodeBytes / 2 : 0) + (pg1 >= 0 ? kCodeBytes / 2 : 0);
             const int64_t a0 = ((int64_t)max(pg0, 0) * p.kv_heads + w.h) * (kCodeBytes / 2);
             const int64_t a1 = ((int64_t)max(pg1, 0) * p.kv_heads + w.h) * (kCodeBytes / 2);
-            ok = wait_for(sh, &sh.kc_empty, (n & 1) ^ 1);
-            ok = __all_sync(0xffffffffu, ok);
+#pragma unroll 1
+            for (int v = 0; v < 2; ++v) {   // K, then V
+                ok = __all_sync(0xffffffffu, wait_for(sh, &sh.c_empty[v], (n & 1) ^ 1));
+                if (!ok) {   // the K codes on their way land before the CTA ends
+                    if (v == 1) tc::mbar_wait(&sh.c_full[0], n & 1, clock64() + tc::kWaitCycles);
+                    break;
+                }
+                if (lane == 0) {
+                    const uint8_t* src = v ? p.v : p.k;
+                    uint8_t* dst = sKc + v * kCodeBytes;
+                    tc::mbar_arrive_expect_tx(&sh.c_full[v], bytes);
+                    if (pg0 >= 0) tc::bulk_g2s(dst, src + a0, kCodeBytes / 2, &sh.c_full[v]);
+                    if (pg1 >= 0) tc::bulk_g2s(dst + kCodeBytes / 2, src + a1, kCodeBytes / 2, &sh.c_full[v]);
+                }
+            }
             if (!ok) break;
-            if (lane == 0) {
-                tc::mbar_arrive_expect_tx(&sh.kc_full, bytes);
-                if (pg0 >= 0) tc::bulk_g2s(sKc, p.k + a0, kCodeBytes / 2, &sh.kc_full);
-                if (pg1 >= 0) tc::bulk_g2s(sKc + kCodeBytes / 2, p.k + a1, kCodeBytes / 2, &sh.kc_full);
-            }
-            ok = wait_for(sh, &sh.vc_empty, (n & 1) ^ 1);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) {   // the K codes on their way land before the CTA ends
-                tc::mbar_wait(&sh.kc_full, n & 1, clock64() + tc::kWaitCycles);
-                break;
-            }
-            if (lane == 0) {
-                tc::mbar_arrive_expect_tx(&sh.vc_full, bytes);
-                if (pg0 >= 0) tc::bulk_g2s(sVc, p.v + a0, kCodeBytes / 2, &sh.vc_full);
-                if (pg1 >= 0) tc::bulk_g2s(sVc + kCodeBytes / 2, p.v + a1, kCodeBytes / 2, &sh.vc_full);
-            }
         }
         if (ok) more = w.next(p);
     }
     // the copies of the last tile have landed before the CTA ends, whatever
     // became of their readers
     if (n > 0) {
-        tc::mbar_wait(&sh.kc_full, (n - 1) & 1, clock64() + tc::kWaitCycles);
-        tc::mbar_wait(&sh.vc_full, (n - 1) & 1, clock64() + tc::kWaitCycles);
+        tc::mbar_wait(&sh.c_full[0], (n - 1) & 1, clock64() + tc::kWaitCycles);
+        tc::mbar_wait(&sh.c_full[1], (n - 1) & 1, clock64() + tc::kWaitCycles);
     }
     if (!ok || !__all_sync(0xffffffffu, wait_for(sh, &sh.info_empty[n % kTiles], ((n / kTiles) & 1) ^ 1))) return;
     if (lane == 0) {
@@ -763,18 +821,18 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
             tc::mbar_init(&sh.info_empty[i], kSoftmaxWarps + kCodeWarps + 1);
         }
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&sh.k_full[i], kCodeWarps);
-            tc::mbar_init(&sh.v_full[i], kCodeWarps);
-            tc::mbar_init(&sh.k_empty[i], 1);
-            tc::mbar_init(&sh.v_empty[i], 1);
+            tc::mbar_init(&sh.full[0][i], kCodeWarps);
+            tc::mbar_init(&sh.full[1][i], kCodeWarps);
+            tc::mbar_init(&sh.empty[0][i], 1);
+            tc::mbar_init(&sh.empty[1][i], 1);
             tc::mbar_init(&sh.s_full[i], 1);
             tc::mbar_init(&sh.p_full[i], kSoftmaxWarps / 2);
             tc::mbar_init(&sh.pv_done[i], 1);
         }
-        tc::mbar_init(&sh.kc_full, 1);
-        tc::mbar_init(&sh.vc_full, 1);
-        tc::mbar_init(&sh.kc_empty, kCodeWarps);
-        tc::mbar_init(&sh.vc_empty, kCodeWarps);
+        tc::mbar_init(&sh.c_full[0], 1);
+        tc::mbar_init(&sh.c_full[1], 1);
+        tc::mbar_init(&sh.c_empty[0], kCodeWarps);
+        tc::mbar_init(&sh.c_empty[1], kCodeWarps);
         tc::mbar_init(&sh.q_full, kSoftmaxWarps);
         tc::mbar_init(&sh.drain, 1);
         sh.failed = 0;
@@ -792,20 +850,19 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
     uint8_t* sV = base + 2 * kTileBytes;
     uint8_t* sQ = base + 4 * kTileBytes;
     uint8_t* sKc = base + 6 * kTileBytes;
-    uint8_t* sVc = sKc + kCodeBytes;
 
     if (warp < kSoftmaxWarps) {
         more_registers<kSoftmaxRegs>();
         softmax_role<MOD>(p, sh, sQ, tmem, warp, lane);
     } else if (warp < kSoftmaxWarps + kCodeWarps) {
         fewer_registers<kCodeRegs>();
-        code_role<CODE>(sh, sK, sV, sKc, sVc, t - 32 * kSoftmaxWarps, lane);
+        code_role<CODE>(sh, sK, sKc, t - 32 * kSoftmaxWarps, lane);
     } else {
         fewer_registers<kOtherRegs>();
         if (warp == kMmaWarp) {
             if (lane == 0) mma_role(sh, sK, sV, sQ, tmem);
         } else if (warp == kWalkWarp) {
-            walk_role(p, sh, sKc, sVc, start_h, left, lane);
+            walk_role(p, sh, sKc, start_h, left, lane);
         }
     }
     __syncwarp();
