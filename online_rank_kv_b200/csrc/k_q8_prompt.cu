@@ -9,27 +9,32 @@
 // accumulator in tensor memory is rescaled a few times per row, not per tile.
 //
 // One CTA per SM holds two tiles of 128 query rows (query tokens x the heads
-// that share a KV head) against key tiles of 128 tokens:
+// that share a KV head) and goes through the keys in steps of one page:
 //   warps 0-3, 4-7  softmax of tile 0 and of tile 1, one thread per row: scores
 //                   from TMEM, weights as fp16 back over them, and the rare
 //                   rescaling; also load, scale and store their own Q rows
 //   warps 8-11      turn codes (shared memory) into fp16 operand tiles
-//   warp 12         one thread issues every MMA: S_i = Q_i K^T, O_i += P_i V
-//   warp 13         walks the CTA's work, looks up pages and scales 16 tiles at
-//                   a time, tells the others about each tile through a ring of
-//                   four descriptions, and copies its codes in (8 KB per page
-//                   and operand by the bulk copy engine)
-// While one tile's softmax runs, the other tile's two products do.  TMEM: S_0,
-// S_1 (fp32, the fp16 weights over their first half), O_0, O_1, 128 columns
-// each.  K and V operand tiles have two buffers each, codes one.
+//   warps 12, 14    issue the MMAs of tile 0 and of tile 1: S_i = Q_i K^T,
+//                   O_i += P_i V
+//   warp 13         walks the CTA's work, looks up pages and scales 32 steps at
+//                   a time, tells the others about each step through a ring of
+//                   eight descriptions, and copies its codes in (8 KB per
+//                   operand by the bulk copy engine)
+// Each tile has two score buffers of 64 columns: a tile's softmax works on one
+// page's scores while the MMAs of the page before (its values, then the scores
+// of the page after next, into the buffer that it frees) run, so neither waits
+// for the other's latency.  TMEM: S_0, S_1 (fp32, two buffers of 64 columns
+// each, the fp16 weights over a buffer's first half), O_0, O_1, 128 columns
+// each.  K and V operand tiles have four buffers each, codes two.
 //
-// Work: (KV head, pair of query tiles, key tile) are numbered through and every
+// Work: (KV head, pair of query tiles, page) are numbered through and every
 // CTA takes an equal contiguous range, so that causal triangles, ragged batches
 // and short chunks on long caches all fill the GPU; a pair that crosses CTAs is
 // joined from its partial sums by a second kernel.
 //
-// Bounds per key tile and pair (148 SMs): 2048 cycles of MMA (64 per
-// instruction, measured alone), 2048 cycles of exponentials (16 per SM and
+// Bounds per 128 keys and pair (148 SMs): 2048 cycles of MMA at the nominal
+// rate (64 per instruction of 128 x 128 x 16), about 3000 at the rate that the
+// chip holds under its power limit; 2048 cycles of exponentials (16 per SM and
 // clock).
 #include "q8_common.cuh"
 #include "tc_util.cuh"
@@ -40,9 +45,11 @@ namespace q8 {
 namespace {
 
 constexpr int kM = 128;                    // query rows per tile
-constexpr int kN = 128;                    // keys per tile
-constexpr int kTileBytes = kN * kHeadDim * 2;   // one fp16 operand tile: 32 KB
-constexpr int kHalf = kTileBytes / 2;      // 64 of its 128 columns: rows of 128 bytes
+constexpr int kN = kPage;                  // keys per step
+// fp16 operand tiles stand as two halves of 64 columns, rows of 128 bytes
+constexpr int kHalf = kN * 128, kTileBytes = 2 * kHalf;     // K, V: 16 KB
+constexpr int kQHalf = kM * 128, kQBytes = 2 * kQHalf;      // Q: 32 KB
+constexpr int kBuffers = 4;                // K and V operand tiles
 constexpr int kSoftmaxWarps = 8, kCodeWarps = 4;
 // Registers per thread, by warpgroup: 2 x 176 + 80 + 80 = 4 x 128, what the
 // launch has.
@@ -51,36 +58,40 @@ constexpr int kSoftmaxRegs = 176, kCodeRegs = 80, kOtherRegs = 80;
 constexpr int kMmaWarp = kSoftmaxWarps + kCodeWarps, kWalkWarp = kMmaWarp + 1;
 constexpr float kShift = 7.f;
 constexpr float kRaise = 8.f;
-// What the start and the end of a pair cost, in key tiles, where work is split.
-constexpr int kPieceTiles = 3;
+// What the start and the end of a pair cost, in steps, where work is split.
+constexpr int kPieceSteps = 8;
 
-// One key tile, as the walking warp describes it.
-constexpr int kFirst = 1, kLast = 2, kEnd = 4;   // of a piece; of the work
-struct Tile {
+// One step, as the walking warp describes it.
+constexpr int kFirst = 1, kEnd = 2;     // of a piece; of the work
+struct Step {
     int flags, key0;
-    int there[2];           // its pages exist
-    float sk[2], lsv[2], isv[2];   // key scale, log2 of the value scale, its inverse
+    int left;               // steps of the piece that follow
+    int there;              // its page exists
+    float sk, lsv, isv;     // key scale, log2 of the value scale, its inverse
     int len, pre, n, first; // the request: tokens, prefix, queries, first query row
     int token0, h;          // the pair's first query, KV head
     int slot;               // partial slot, -1: the piece is the whole pair
 };
-constexpr int kTiles = 4;
+constexpr int kSteps = 8;
 
 struct Shared {
-    Tile tile[kTiles];
-    uint64_t info_full[kTiles], info_empty[kTiles];
-    uint64_t c_full[2], c_empty[2];           // codes of K, of V
-    uint64_t full[2][2], empty[2][2];         // operand tiles of K, of V: two buffers each
-    uint64_t q_full, s_full[2], p_full[2], pv_done[2], drain;
+    Step step[kSteps];
+    uint64_t info_full[kSteps], info_empty[kSteps];
+    uint64_t c_full[2][2], c_empty[2][2];                 // codes of K, of V
+    uint64_t full[2][kBuffers], empty[2][kBuffers];       // operand tiles of K, of V
+    uint64_t q_full[2], s_full[2][2], p_full[2][2], drain[2];
+    // Even and odd steps apart: a softmax may be a step ahead of its values'
+    // product, and a parity tells only neighbouring phases apart.
+    uint64_t pv_done[2][2];
     uint32_t tmem;
     int failed;
     int64_t scan[16];
     int64_t start_off;
     int start_b, start_pair;
 };
-constexpr int kCodeBytes = kN * kHeadDim;   // K or V codes of a tile: 16 KB
-// dynamic shared memory: 1024-byte aligned [K 2 tiles][V 2 tiles][Q 2 tiles][K codes][V codes]
-constexpr int kSmemBytes = 6 * kTileBytes + 2 * kCodeBytes + 1024;
+constexpr int kCodeBytes = kN * kHeadDim;   // K or V codes of a step: 8 KB
+// dynamic shared memory: 1024-byte aligned [K tiles][V tiles][Q 2 tiles][K codes 2][V codes 2]
+constexpr int kSmemBytes = 2 * kBuffers * kTileBytes + 2 * kQBytes + 4 * kCodeBytes + 1024;
 
 template <int N>
 __device__ __forceinline__ void more_registers() {
@@ -102,6 +113,25 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
           "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(taddr));
 }
+// Waits for this thread's TMEM loads.  The registers that they fill pass through
+// the wait, so that no use of them can be moved in front of it.
+__device__ __forceinline__ void tmem_wait(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                   "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                   "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :
+                 : "memory");
+}
+
 // Two fp32 operations per instruction.
 __device__ __forceinline__ uint64_t pair(float x, float y) {
     uint64_t r;
@@ -154,11 +184,11 @@ __device__ __forceinline__ bool wait_for(Shared& sh, uint64_t* bar, uint32_t par
     return tc::mbar_try_wait(bar, parity) || wait_longer(sh, bar, parity);
 }
 
-// The key tiles that a pair of query tiles sees.
+// The steps that a pair of query tiles sees.
 struct Span {
     int p0;            // position of the pair's first query
-    int a, lo, tiles;
-    __device__ __forceinline__ int tile_of(int i) const { return i < a ? i : i - a + lo; }
+    int a, lo, steps;
+    __device__ __forceinline__ int step_of(int i) const { return i < a ? i : i - a + lo; }
 };
 __device__ __forceinline__ Span span_of(const AttnArgs& p, const Seen<kN>& r, int pair) {
     Span s;
@@ -172,12 +202,12 @@ __device__ __forceinline__ Span span_of(const AttnArgs& p, const Seen<kN>& r, in
     if (pre >= s.lo) {
         s.a = 0;
         s.lo = 0;
-        s.tiles = max(pre, hi);
+        s.steps = max(pre, hi);
     } else {
         s.a = pre;
-        s.tiles = pre + max(0, hi - s.lo);
+        s.steps = pre + max(0, hi - s.lo);
     }
-    if (s.tiles == 0) s.tiles = 1;   // nothing to see: one hidden tile, so that zeros are written
+    if (s.steps == 0) s.steps = 1;   // nothing to see: one hidden step, so that zeros are written
     return s;
 }
 
@@ -187,20 +217,20 @@ __device__ __forceinline__ int pairs_of(const AttnArgs& p, int b) {
     return c1 > c0 ? (int)((c1 - c0 + 2 * p.tq - 1) / (2 * p.tq)) : 0;
 }
 
-// A CTA's run through (head, request, pair, tile).  A pair costs its tiles and
-// kPieceTiles, which stand in front of them.
+// A CTA's run through (head, request, pair, step).  A pair costs its steps and
+// kPieceSteps, which stand in front of them.
 struct Walk {
     int h, b, pair, pairs;
-    int t0, t1;             // key tiles of the present piece: [t0, t1) of span.tiles
+    int t0, t1;             // the present piece: steps [t0, t1) of span.steps
     int64_t left;           // cost still to spend, this piece's included
     Seen<kN> r;
     Span span;
-    // the piece from cost offset `off` of the pair on; false: no tile of it is this CTA's
+    // the piece from cost offset `off` of the pair on; false: no step of it is this CTA's
     __device__ __forceinline__ bool cut(int64_t off) {
-        const int64_t end = off + left - kPieceTiles;
-        t0 = off > kPieceTiles ? (int)(off - kPieceTiles) : 0;
-        t1 = (int)(end < span.tiles ? end : span.tiles);
-        left -= span.tiles + kPieceTiles - off;
+        const int64_t end = off + left - kPieceSteps;
+        t0 = off > kPieceSteps ? (int)(off - kPieceSteps) : 0;
+        t1 = (int)(end < span.steps ? end : span.steps);
+        left -= span.steps + kPieceSteps - off;
         return t1 > t0;
     }
     __device__ __forceinline__ bool start(const AttnArgs& p, int h_, int b_, int pair_, int64_t off, int64_t n) {
@@ -248,249 +278,259 @@ template <bool MOD>
 __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint8_t* sQ, uint32_t tmem, int warp, int lane) {
     const int i = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t quad = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + i * kN + quad, tO = tmem + 2 * kN + i * kHeadDim + quad;
+    const uint32_t tS = tmem + i * 2 * kN + quad, tO = tmem + 4 * kN + i * kHeadDim + quad;
     const int k = row / p.g, hg = row % p.g;
-    float rowf = 0.f, slope = 0.f, M = -INFINITY, l = 0.f;
-    int pos = 0, see_from = -1, token = 0, head = 0;
-    int wp_min = 0, wp_max = 0;
+    const int c16 = lane & 15, up16 = lane >> 4;
+    uint8_t* const q_rows = sQ + i * kQBytes + (warp & 3) * 32 * 128;   // the warp's rows, both halves
+
+    int token = 0, head = 0;
     bool on = false;
+    uint4 x[16];   // the warp's queries: two rows per load, 16 lanes a row
+    auto load = [&](const Step& st) {
+        token = st.token0 + i * p.tq + k;
+        head = st.h * p.g + hg;
+        on = k < p.tq && token < st.n;
+        const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)st.first * p.q_stride + c16 * 8;
+        const int64_t own = on ? (int64_t)token * p.q_stride + head * kHeadDim : -1;
+#pragma unroll
+        for (int z = 0; z < 16; ++z) {
+            const int64_t src = __shfl_sync(0xffffffffu, own, 2 * z + up16);
+            x[z] = src >= 0 ? __ldg(reinterpret_cast<const uint4*>(q0 + src)) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    {
+        const bool ok = __all_sync(0xffffffffu, wait_for(sh, &sh.info_full[0], 0));
+        if (!ok || (sh.step[0].flags & kEnd)) return;
+        load(sh.step[0]);
+    }
 
-    for (int n = 0;; ++n) {
-        const Tile& ti = sh.tile[n % kTiles];
-        bool ok = wait_for(sh, &sh.info_full[n % kTiles], (n / kTiles) & 1);
-        const int flags = ok ? ti.flags : kEnd;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok || (flags & kEnd)) return;
-
-        if (flags & kFirst) {   // the warp's 32 queries, two rows per load, 16 lanes a row
-            token = ti.token0 + i * p.tq + k;
-            head = ti.h * p.g + hg;
-            on = k < p.tq && token < ti.n;
-            // (rolled: straight-line code that runs once per piece costs more in
-            // instruction fetches than it saves)
-            const int c = lane & 15;
-            const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)ti.first * p.q_stride + c * 8;
-            int64_t at = on ? (int64_t)token * p.q_stride + head * kHeadDim : -1;   // of this thread's row
-#pragma unroll 1
-            for (int b = 0; b < 2; ++b) {
-                uint4 x[8];
+    for (int n = 0;;) {   // pieces
+        // ---- queries ----
+        float rowf = 0.f;
 #pragma unroll
-                for (int z = 0; z < 8; ++z) {
-                    const int64_t src = __shfl_sync(0xffffffffu, at, b * 16 + 2 * z + (lane >> 4));
-                    x[z] = src >= 0 ? __ldg(reinterpret_cast<const uint4*>(q0 + src)) : make_uint4(0u, 0u, 0u, 0u);
-                }
+        for (int z = 0; z < 16; ++z) {
+            const int r32 = 2 * z + up16;
+            const uint32_t v[4] = {x[z].x, x[z].y, x[z].z, x[z].w};
+            // bf16 magnitudes order like their bits: the row's largest exponent
+            uint32_t top = __vmaxu2(__vmaxu2(v[0] & 0x7fff7fffu, v[1] & 0x7fff7fffu),
+                                    __vmaxu2(v[2] & 0x7fff7fffu, v[3] & 0x7fff7fffu));
+            top = max(top >> 16, top & 0xffffu);
 #pragma unroll
-                for (int z = 0; z < 8; ++z) {
-                    const int r32 = b * 16 + 2 * z + (lane >> 4);
-                    const uint32_t v[4] = {x[z].x, x[z].y, x[z].z, x[z].w};
-                    // bf16 magnitudes order like their bits: the row's largest exponent
-                    uint32_t top = __vmaxu2(__vmaxu2(v[0] & 0x7fff7fffu, v[1] & 0x7fff7fffu),
-                                            __vmaxu2(v[2] & 0x7fff7fffu, v[3] & 0x7fff7fffu));
-                    top = max(top >> 16, top & 0xffffu);
-                    const uint32_t half = lane < 16 ? 0x0000ffffu : 0xffff0000u;
-                    top = __reduce_max_sync(half, top);
-                    // 2^up brings the row's largest element into [2^14, 2^15)
-                    const int up = max(-126, min(126, 14 - ((int)(top >> 7) - 127)));
-                    const float f = __uint_as_float((uint32_t)(up + 127) << 23);
-                    uint32_t o[4];
+            for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            // 2^up brings the row's largest element into [2^14, 2^15)
+            const int up = max(-126, min(126, 14 - ((int)(top >> 7) - 127)));
+            const float f = __uint_as_float((uint32_t)(up + 127) << 23);
+            uint32_t o[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const __half2 hh = __floats2half2_rn(__uint_as_float(v[e] << 16) * f,
-                                                             __uint_as_float(v[e] & 0xffff0000u) * f);
-                        o[e] = *reinterpret_cast<const uint32_t*>(&hh);
-                    }
-                    *reinterpret_cast<uint4*>(sQ + i * kTileBytes + (c >> 3) * kHalf + ((warp & 3) * 32 + r32) * 128 +
-                                              (((c & 7) ^ (r32 & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    // the row's own thread keeps 2^-up
-                    const int mine = __shfl_sync(0xffffffffu, up, (lane & 1) << 4);
-                    if ((lane & ~1) == b * 16 + 2 * z)
-                        rowf = __uint_as_float((uint32_t)(127 - mine) << 23) * (p.scale * (MOD ? 1.f : kLog2e));
-                }
+            for (int e = 0; e < 4; ++e) {
+                const __half2 hh = __floats2half2_rn(__uint_as_float(v[e] << 16) * f, __uint_as_float(v[e] & 0xffff0000u) * f);
+                o[e] = *reinterpret_cast<const uint32_t*>(&hh);
             }
-            tc::fence_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sh.q_full);
-            pos = ti.len - ti.n + min(token, ti.n - 1);
-            see_from = p.window > 0 ? max(-1, pos - p.window) : -1;   // sees (see_from, pos] and the prefix
-            if (MOD) slope = p.slopes && on ? p.slopes[head] * kLog2e : 0.f;
-            wp_min = __reduce_min_sync(0xffffffffu, pos);
-            wp_max = __reduce_max_sync(0xffffffffu, pos);
-            M = -INFINITY;
-            l = 0.f;
+            *reinterpret_cast<uint4*>(q_rows + (c16 >> 3) * kQHalf + r32 * 128 + (((c16 & 7) ^ (r32 & 7)) << 4)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+            // the row's own thread keeps 2^-up
+            const int mine = __shfl_sync(0xffffffffu, up, (lane & 1) << 4);
+            if ((lane >> 1) == z)
+                rowf = __uint_as_float((uint32_t)(127 - mine) << 23) * (p.scale * (MOD ? 1.f : kLog2e));
         }
-
-        const int key0 = ti.key0, len = ti.len, pre = ti.pre;
-        const bool clear = ti.there[0] && ti.there[1] && key0 + kN <= len &&
-                           ((key0 + kN - 1 <= wp_min && (p.window == 0 || key0 > wp_max - p.window)) || key0 + kN <= pre);
-        // the smallest normal number in place of zero keeps hidden scores at -inf
-        float a0 = fmaxf(rowf * ti.sk[0], 1.17549435e-38f), a1 = fmaxf(rowf * ti.sk[1], 1.17549435e-38f);
-        ok = __all_sync(0xffffffffu, wait_for(sh, &sh.s_full[i], n & 1));
-        if (!ok) return;
-        tc::tc_fence_after();
-        uint32_t s[kN];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
-        tc::tmem_wait_ld();
-        if (MOD) {
-            const float d0 = (float)(pos - key0);
-#pragma unroll
-            for (int e = 0; e < kN; ++e) {
-                float x = __uint_as_float(s[e]) * (e < kPage ? a0 : a1);
-                if (p.cap > 0.f) x = p.cap * tanh_abs(__fdividef(x, p.cap));
-                s[e] = __float_as_uint(x * kLog2e - slope * fabsf(d0 - (float)e));
-            }
-            a0 = a1 = 1.f;
-        }
-        if (!clear) {
-            const bool there0 = ti.there[0], there1 = ti.there[1];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int k0 = key0 + 32 * c;
-                uint32_t m = (bits(see_from + 1 - k0, pos + 1 - k0) | bits(0, pre - k0)) & bits(0, len - k0);
-                if (!(c < 2 ? there0 : there1)) m = 0u;
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (!((m >> e) & 1u)) s[32 * c + e] = 0xff800000u;   // -inf
-            }
-        }
-        // ---- the row's maximum ----
-        float t0 = -INFINITY, t1 = -INFINITY;
-        {
-            float m[8];
-#pragma unroll
-            for (int z = 0; z < 8; ++z) m[z] = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < kN; e += 2) {
-                const int z = (e >> 1) & 3;
-                float& r = m[e < kPage ? z : 4 + z];
-                r = max3(r, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-            }
-            t0 = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-            t1 = fmaxf(fmaxf(m[4], m[5]), fmaxf(m[6], m[7]));
-        }
-        const float lsv0 = ti.lsv[0], lsv1 = ti.lsv[1];
-        const float now = fmaxf(fmaf(t0, a0, lsv0), fmaf(t1, a1, lsv1));
-        const bool raise = now > M + kRaise || (M == -INFINITY && now > -INFINITY);
-        if (__any_sync(0xffffffffu, raise)) {
-            const float f = raise && M > -INFINITY ? ex2(M - now) : 1.f;
-            if (raise) M = now;
-            l *= f;
-            if (!(flags & kFirst)) {   // the accumulator holds earlier tiles
-                ok = __all_sync(0xffffffffu, wait_for(sh, &sh.pv_done[i], (n - 1) & 1));
-                if (!ok) return;
-                tc::tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < 8; ++c) {
-                    uint32_t o[16];
-                    tc::tmem_ld16(tO + 16 * c, o);
-                    tc::tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                    tc::tmem_st16(tO + 16 * c, o);
-                }
-            }
-        }
-        // ---- weights ----
-        // One fused multiply-add per weight: x - M with x unrounded, M and
-        // M - log2 s_v rounded, off by 2^-24 |M| between pages.  From
-        // |M| = 2^10 on, x is rounded like M was first, so that the row's
-        // largest key gives exactly x - M = 0.
-        const float Mb = M == -INFINITY ? 0.f : M;
-        float b0 = lsv0 + (kShift - Mb), b1 = lsv1 + (kShift - Mb);
-        if (__any_sync(0xffffffffu, fabsf(Mb) >= 1024.f)) {
-#pragma unroll
-            for (int e = 0; e < kN; ++e)
-                s[e] = __float_as_uint(fmaf(__uint_as_float(s[e]), e < kPage ? a0 : a1, e < kPage ? lsv0 : lsv1) - Mb);
-            a0 = a1 = 1.f;
-            b0 = b1 = kShift;
-        }
-        const uint64_t aa[2] = {pair(a0, a0), pair(a1, a1)}, bb[2] = {pair(b0, b0), pair(b1, b1)};
-        uint64_t sum[2] = {0, 0};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            uint32_t o[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                float2 x = split(fma2(s[32 * c + e], s[32 * c + e + 1], aa[c >> 1], bb[c >> 1]));
-                x.x = ex2(x.x);
-                x.y = ex2(x.y);
-                sum[c >> 1] = add2(sum[c >> 1], pair(x.x, x.y));
-                const __half2 hh = __floats2half2_rn(x.x, x.y);
-                o[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
-            }
-            tc::tmem_st16(tS + 16 * c, o);
-        }
-        const float2 s0 = split(sum[0]), s1 = split(sum[1]);
-        l += (s0.x + s0.y) * ti.isv[0] + (s1.x + s1.y) * ti.isv[1];
-        tc::tmem_wait_st();
-        tc::tc_fence_before();
+        tc::fence_async_smem();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sh.p_full[i]);
+        if (lane == 0) tc::mbar_arrive(&sh.q_full[i]);
 
-        if (flags & kLast) {   // end of the piece
-            ok = __all_sync(0xffffffffu, wait_for(sh, &sh.pv_done[i], n & 1));
+        const int n_q = sh.step[n % kSteps].n, len = sh.step[n % kSteps].len, pre = sh.step[n % kSteps].pre;
+        const int pos = len - n_q + min(token, n_q - 1);
+        const int see_from = p.window > 0 ? max(-1, pos - p.window) : -1;   // sees (see_from, pos] and the prefix
+        const float slope = MOD && p.slopes && on ? p.slopes[head] * kLog2e : 0.f;
+        const int wp_min = __reduce_min_sync(0xffffffffu, pos), wp_max = __reduce_max_sync(0xffffffffu, pos);
+        float M = -INFINITY, l = 0.f;
+
+        for (bool first = true;; first = false) {   // steps
+            const Step& st = sh.step[n % kSteps];
+            bool ok = wait_for(sh, &sh.info_full[n % kSteps], (n / kSteps) & 1) &&
+                      wait_for(sh, &sh.s_full[i][n & 1], (n >> 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
             tc::tc_fence_after();
-            const int slot = ti.slot;
-            const int64_t at = (int64_t)slot * (2 * kM) + i * kM + row;
-            const float inv = l > 0.f ? __fdiv_rn(1.f, l) : (l == 0.f ? 0.f : l);
-            // through the warp's own Q rows (their products are done), so that whole
-            // rows are written: a row's thread puts 64 bytes at a time in its row's
-            // two halves, then 16 lanes write a row of bf16, 32 lanes one of fp32
-            uint8_t* const mine = sQ + i * kTileBytes + (warp & 3) * 32 * 128;
+            const uint32_t tSn = tS + (n & 1) * kN;
+            uint32_t s[kN];
+            tmem_ld32(tSn, *reinterpret_cast<uint32_t(*)[32]>(s));
+            tmem_ld32(tSn + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+            const int key0 = st.key0;
+            const bool there = st.there;
+            const bool clear = there && key0 + kN <= len &&
+                               ((key0 + kN - 1 <= wp_min && (p.window == 0 || key0 > wp_max - p.window)) || key0 + kN <= pre);
+            // the smallest normal number in place of zero keeps hidden scores at -inf
+            float a = fmaxf(rowf * st.sk, 1.17549435e-38f);
+            const float lsv = st.lsv;
+            tmem_wait(*reinterpret_cast<uint32_t(*)[32]>(s));
+            tmem_wait(*reinterpret_cast<uint32_t(*)[32]>(s + 32));
+            if (MOD) {
+                const float d0 = (float)(pos - key0);
+#pragma unroll
+                for (int e = 0; e < kN; ++e) {
+                    float y = __uint_as_float(s[e]) * a;
+                    if (p.cap > 0.f) y = p.cap * tanh_abs(__fdividef(y, p.cap));
+                    s[e] = __float_as_uint(y * kLog2e - slope * fabsf(d0 - (float)e));
+                }
+                a = 1.f;
+            }
+            if (!clear) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int k0 = key0 + 32 * c;
+                    uint32_t m = (bits(see_from + 1 - k0, pos + 1 - k0) | bits(0, pre - k0)) & bits(0, len - k0);
+                    if (!there) m = 0u;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (!((m >> e) & 1u)) s[32 * c + e] = 0xff800000u;   // -inf
+                }
+            }
+            // ---- the row's maximum ----
+            float top;
+            {
+                float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int e = 0; e < kN; e += 2)
+                    m[(e >> 1) & 3] = max3(m[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+            }
+            const float now = fmaf(top, a, lsv);
+            const bool raise = now > M + kRaise || (M == -INFINITY && now > -INFINITY);
+            if (__any_sync(0xffffffffu, raise)) {
+                const float f = raise && M > -INFINITY ? ex2(M - now) : 1.f;
+                if (raise) M = now;
+                l *= f;
+                if (!first) {   // the accumulator holds earlier steps
+                    ok = __all_sync(0xffffffffu, wait_for(sh, &sh.pv_done[i][(n - 1) & 1], ((n - 1) >> 1) & 1));
+                    if (!ok) return;
+                    tc::tc_fence_after();
 #pragma unroll 1
-            for (int part = 0; part < 2; ++part) {   // 64 of the 128 columns
-                uint32_t o[64];
-                __syncwarp();
-                tmem_ld32(tO + 64 * part, *reinterpret_cast<uint32_t(*)[32]>(o));
-                tmem_ld32(tO + 64 * part + 32, *reinterpret_cast<uint32_t(*)[32]>(o + 32));
-                tc::tmem_wait_ld();
-                if (slot < 0) {
-#pragma unroll
                     for (int c = 0; c < 8; ++c) {
-                        uint32_t v[4];
+                        uint32_t o[16];
+                        tc::tmem_ld16(tO + 16 * c, o);
+                        tmem_wait(o);
 #pragma unroll
-                        for (int z = 0; z < 4; ++z) {
-                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * c + 2 * z]) * inv,
-                                                                            __uint_as_float(o[8 * c + 2 * z + 1]) * inv);
-                            v[z] = *reinterpret_cast<const uint32_t*>(&b2);
-                        }
-                        *reinterpret_cast<uint4*>(mine + part * kHalf + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-                            make_uint4(v[0], v[1], v[2], v[3]);
-                    }
-                    if (part == 0) continue;
-                    __syncwarp();
-                    const int c = lane & 15;
-                    __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(p.out) + c * 8;
-                    const int64_t own = on ? ((int64_t)(ti.first + token) * p.kv_heads * p.g + head) * kHeadDim : -1;
-#pragma unroll 2
-                    for (int z = 0; z < 16; ++z) {
-                        const int r32 = 2 * z + (lane >> 4);
-                        const uint4 v = *reinterpret_cast<const uint4*>(mine + (c >> 3) * kHalf + r32 * 128 + (((c & 7) ^ (r32 & 7)) << 4));
-                        const int64_t to = __shfl_sync(0xffffffffu, own, r32);
-                        if (to >= 0) *reinterpret_cast<uint4*>(out + to) = v;
-                    }
-                } else {   // fp32: 64 columns are 256 bytes, 128 in each half
-#pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        *reinterpret_cast<uint4*>(mine + (c >> 3) * kHalf + lane * 128 + (((c & 7) ^ (lane & 7)) << 4)) =
-                            make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-                    __syncwarp();
-                    const int c = lane & 15;
-#pragma unroll 2
-                    for (int z = 0; z < 16; ++z) {
-                        const int r32 = 2 * z + (lane >> 4);
-                        const uint4 v = *reinterpret_cast<const uint4*>(mine + (c >> 3) * kHalf + r32 * 128 + (((c & 7) ^ (r32 & 7)) << 4));
-                        *reinterpret_cast<uint4*>(p.part + ((int64_t)slot * (2 * kM) + i * kM + (warp & 3) * 32 + r32) * kHeadDim +
-                                                  64 * part + 4 * c) = v;
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tc::tmem_st16(tO + 16 * c, o);
                     }
                 }
             }
-            if (slot >= 0 && on) *reinterpret_cast<float2*>(p.ml + at * 2) = make_float2(M, l);
+            // ---- weights ----
+            // One fused multiply-add per weight: x - M with x unrounded, M and
+            // M - log2 s_v rounded, off by 2^-24 |M| between pages.  From
+            // |M| = 2^10 on, x is rounded like M was first, so that the row's
+            // largest key gives exactly x - M = 0.
+            const float Mb = M == -INFINITY ? 0.f : M;
+            float b = lsv + (kShift - Mb);
+            if (__any_sync(0xffffffffu, fabsf(Mb) >= 1024.f)) {
+#pragma unroll
+                for (int e = 0; e < kN; ++e) s[e] = __float_as_uint(fmaf(__uint_as_float(s[e]), a, lsv) - Mb);
+                a = 1.f;
+                b = kShift;
+            }
+            const uint64_t aa = pair(a, a), bb = pair(b, b);
+            uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t o[16];
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    float2 y = split(fma2(s[32 * c + e], s[32 * c + e + 1], aa, bb));
+                    y.x = ex2(y.x);
+                    y.y = ex2(y.y);
+                    if (e & 2) sum1 = add2(sum1, pair(y.x, y.y));
+                    else sum0 = add2(sum0, pair(y.x, y.y));
+                    const __half2 hh = __floats2half2_rn(y.x, y.y);
+                    o[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
+                }
+                tc::tmem_st16(tSn + 16 * c, o);
+            }
+            const float2 s2 = split(add2(sum0, sum1));
+            l += (s2.x + s2.y) * st.isv;
+            const int left = st.left;
+            tc::tmem_wait_st();
             tc::tc_fence_before();
             __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sh.p_full[i][n & 1]);
+            if (left == 0) break;
+            if (lane == 0) tc::mbar_arrive(&sh.info_empty[n % kSteps]);
+            ++n;
         }
-        if (lane == 0) tc::mbar_arrive(&sh.info_empty[n % kTiles]);
+
+        // ---- end of the piece; the next one's queries are loaded meanwhile ----
+        const Step& st = sh.step[n % kSteps];
+        const int slot = st.slot;
+        const int64_t own = on ? ((int64_t)(st.first + token) * p.kv_heads * p.g + head) * kHeadDim : -1;
+        const bool own_on = on;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sh.info_empty[n % kSteps]);
+        const int nx = n + 1;
+        bool ok = __all_sync(0xffffffffu, wait_for(sh, &sh.info_full[nx % kSteps], (nx / kSteps) & 1));
+        if (!ok) return;
+        const bool more = !(sh.step[nx % kSteps].flags & kEnd);
+        if (more) load(sh.step[nx % kSteps]);
+        ok = __all_sync(0xffffffffu, wait_for(sh, &sh.pv_done[i][n & 1], (n >> 1) & 1));
+        if (!ok) return;
+        tc::tc_fence_after();
+        const float inv = l > 0.f ? __fdiv_rn(1.f, l) : (l == 0.f ? 0.f : l);
+        // Through the warp's own Q rows (their products are done), so that whole
+        // rows are written: a row's thread puts its columns there 32 at a time
+        // (bf16: all of them, then 16 lanes write a row; fp32: 32 columns, then 8
+        // lanes write a row's 128 bytes).
+        if (slot < 0) {
+#pragma unroll 1
+            for (int part = 0; part < 4; ++part) {
+                uint32_t o[32];
+                tmem_ld32(tO + 32 * part, o);
+                tmem_wait(o);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t v[4];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * c + 2 * z]) * inv,
+                                                                        __uint_as_float(o[8 * c + 2 * z + 1]) * inv);
+                        v[z] = *reinterpret_cast<const uint32_t*>(&b2);
+                    }
+                    *reinterpret_cast<uint4*>(q_rows + (part >> 1) * kQHalf + lane * 128 + (((4 * (part & 1) + c) ^ (lane & 7)) << 4)) =
+                        make_uint4(v[0], v[1], v[2], v[3]);
+                }
+            }
+            __syncwarp();
+            __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(p.out) + c16 * 8;
+#pragma unroll 2
+            for (int z = 0; z < 16; ++z) {
+                const int r32 = 2 * z + up16;
+                const uint4 v = *reinterpret_cast<const uint4*>(q_rows + (c16 >> 3) * kQHalf + r32 * 128 + (((c16 & 7) ^ (r32 & 7)) << 4));
+                const int64_t to = __shfl_sync(0xffffffffu, own, r32);
+                if (to >= 0) *reinterpret_cast<uint4*>(out + to) = v;
+            }
+        } else {
+            const int64_t at = (int64_t)slot * (2 * kM) + i * kM + (warp & 3) * 32;
+#pragma unroll 1
+            for (int part = 0; part < 4; ++part) {
+                uint32_t o[32];
+                __syncwarp();
+                tmem_ld32(tO + 32 * part, o);
+                tmem_wait(o);
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    *reinterpret_cast<uint4*>(q_rows + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                        make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                __syncwarp();
+#pragma unroll 2
+                for (int z = 0; z < 8; ++z) {
+                    const int r32 = 4 * z + (lane >> 3), c = lane & 7;
+                    const uint4 v = *reinterpret_cast<const uint4*>(q_rows + r32 * 128 + ((c ^ (r32 & 7)) << 4));
+                    *reinterpret_cast<uint4*>(p.part + (at + r32) * kHeadDim + 32 * part + 4 * c) = v;
+                }
+            }
+            if (own_on) *reinterpret_cast<float2*>(p.ml + (at + lane) * 2) = make_float2(M, l);
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (!more) return;
+        n = nx;
     }
 }
 
@@ -500,21 +540,21 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
 // the neighbouring row: its swizzle differs in the lowest bit, so the 8 stores
 // go to different banks.
 template <int CODE>
-__device__ __forceinline__ void code_tile(uint8_t* tile, const uint8_t* codes, int u, int rows0, int rows1) {
+__device__ __forceinline__ void code_tile(uint8_t* tile, const uint8_t* codes, int u, int rows) {
     const int c = u & 7, row0 = (u >> 3) ^ (c >> 2), c0 = 2 * (c & 3);
-    uint4 x[8];
+    uint4 x[4];
 #pragma unroll
-    for (int s = 0; s < 8; ++s) x[s] = *reinterpret_cast<const uint4*>(codes + (s * 16 + row0) * kHeadDim + c * 16);
-    if (rows0 < kPage || rows1 < kPage) {   // behind the last token, or a page that is not there
+    for (int s = 0; s < 4; ++s) x[s] = *reinterpret_cast<const uint4*>(codes + (s * 16 + row0) * kHeadDim + c * 16);
+    if (rows < kN) {   // behind the last token, or a page that is not there
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
-            if (((s * 16 + row0) & (kPage - 1)) >= (s < 4 ? rows0 : rows1)) x[s] = make_uint4(0u, 0u, 0u, 0u);
+        for (int s = 0; s < 4; ++s)
+            if (s * 16 + row0 >= rows) x[s] = make_uint4(0u, 0u, 0u, 0u);
     }
     uint8_t* const to = tile + (c >> 2) * kHalf + row0 * 128;
     uint8_t* const to0 = to + ((c0 ^ (row0 & 7)) << 4);
     uint8_t* const to1 = to + (((c0 + 1) ^ (row0 & 7)) << 4);
 #pragma unroll
-    for (int s = 0; s < 8; ++s) {
+    for (int s = 0; s < 4; ++s) {
         const uint32_t v[4] = {Codes<CODE>::bias(x[s].x), Codes<CODE>::bias(x[s].y), Codes<CODE>::bias(x[s].z),
                                Codes<CODE>::bias(x[s].w)};
         *reinterpret_cast<uint4*>(to0 + s * 2048) =
@@ -527,86 +567,99 @@ __device__ __forceinline__ void code_tile(uint8_t* tile, const uint8_t* codes, i
 template <int CODE>
 __device__ __forceinline__ void code_role(Shared& sh, uint8_t* sK, const uint8_t* sKc, int u, int lane) {
     for (int n = 0;; ++n) {
-        const Tile& ti = sh.tile[n % kTiles];
-        if (!wait_for(sh, &sh.info_full[n % kTiles], (n / kTiles) & 1) || (ti.flags & kEnd)) return;
-        const int rows = ti.len - ti.key0;
-        const int rows0 = ti.there[0] ? min(kPage, rows) : 0, rows1 = ti.there[1] ? min(kPage, rows - kPage) : 0;
-        const int st = n & 1;
-        const uint32_t par = (n >> 1) & 1;
+        const Step& st = sh.step[n % kSteps];
+        if (!wait_for(sh, &sh.info_full[n % kSteps], (n / kSteps) & 1) || (st.flags & kEnd)) return;
+        const int rows = st.there ? st.len - st.key0 : 0;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sh.info_empty[n % kSteps]);
+        const int bf = n % kBuffers;
 #pragma unroll 1
         for (int v = 0; v < 2; ++v) {   // K, then V
-            if (!wait_for(sh, &sh.c_full[v], n & 1) || !wait_for(sh, &sh.empty[v][st], par ^ 1)) return;
-            code_tile<CODE>(sK + (2 * v + st) * kTileBytes, sKc + v * kCodeBytes, u, rows0, rows1);
+            if (!wait_for(sh, &sh.c_full[v][n & 1], (n >> 1) & 1) ||
+                !wait_for(sh, &sh.empty[v][bf], ((n / kBuffers) & 1) ^ 1))
+                return;
+            code_tile<CODE>(sK + (kBuffers * v + bf) * kTileBytes, sKc + (2 * v + (n & 1)) * kCodeBytes, u, rows);
             tc::fence_async_smem();
             __syncwarp();
             if (lane == 0) {
-                tc::mbar_arrive(&sh.full[v][st]);
-                tc::mbar_arrive(&sh.c_empty[v]);
+                tc::mbar_arrive(&sh.full[v][bf]);
+                tc::mbar_arrive(&sh.c_empty[v][n & 1]);
             }
         }
-        if (lane == 0) tc::mbar_arrive(&sh.info_empty[n % kTiles]);
     }
 }
 
-// =================== MMA (one thread) =======================================
-__device__ __forceinline__ void mma_role(Shared& sh, const uint8_t* sK, const uint8_t* sV, const uint8_t* sQ, uint32_t tmem) {
+// =================== MMA ====================================================
+// The whole warp runs this and one lane issues: the descriptors then stay in
+// uniform registers (a branch for one lane around it all costs 100 cycles per
+// MMA beside the other warps, against the 64 that the MMA itself takes).
+__device__ __forceinline__ bool elect() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Tile i's MMAs.  A step's description is read where a piece begins only: the
+// walk cannot overwrite it before, since this step's softmax has not run.
+__device__ __forceinline__ void mma_role(Shared& sh, uint32_t aK, uint32_t aQ, uint32_t tmem, int i) {
     constexpr uint32_t idS = tc::idesc_f32acc(0, kM, kN, 0, 0), idO = tc::idesc_f32acc(0, kM, kHeadDim, 0, 1);
-    const uint64_t dK = desc_sw128(tc::smem_u32(sK), 16, 1024), dQ = desc_sw128(tc::smem_u32(sQ), 16, 1024);
-    const uint64_t dV = desc_sw128(tc::smem_u32(sV), kHalf, 1024);
-    // descriptors step in units of 16 bytes
-    auto scores = [&](int i, int st) {
-        const uint64_t a = dQ + i * (kTileBytes >> 4), b = dK + st * (kTileBytes >> 4);
+    const uint64_t dK = desc_sw128(aK, 16, 1024), dQ = desc_sw128(aQ + i * kQBytes, 16, 1024);
+    const uint64_t dV = desc_sw128(aK + kBuffers * kTileBytes, kHalf, 1024);
+    const uint32_t tS = tmem + 2 * i * kN, tO = tmem + 4 * kN + i * kHeadDim;
+    const bool leader = elect();   // one lane for all: a commit covers its own thread's MMAs
+    auto waited = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_for(sh, bar, parity)); };
+    // scores of step n (descriptors step in units of 16 bytes); false: a wait gave up
+    auto scores = [&](int n) {
+        const int bf = n % kBuffers;
+        if (!waited(&sh.full[0][bf], (n / kBuffers) & 1)) return false;
+        tc::tc_fence_after();
+        const uint64_t b = dK + bf * (kTileBytes >> 4);
+        if (leader) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int o = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-            tc::mma_f16_ss(tmem + i * kN, a + o, b + o, idS, k > 0);
+            for (int k = 0; k < 8; ++k)
+                tc::mma_f16_ss(tS + (n & 1) * kN, dQ + (((k >> 2) * kQHalf + (k & 3) * 32) >> 4),
+                               b + (((k >> 2) * kHalf + (k & 3) * 32) >> 4), idS, k > 0);
+            tc::mma_commit(&sh.s_full[i][n & 1]);
+            tc::mma_commit(&sh.empty[0][bf]);
         }
-        tc::mma_commit(&sh.s_full[i]);
+        __syncwarp();
+        return true;
     };
-    auto values = [&](int i, int st, uint32_t more) {
-        const uint64_t b = dV + st * (kTileBytes >> 4);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            tc::mma_f16_ts(tmem + 2 * kN + i * kHeadDim, tmem + i * kN + k * 8, b + k * (2048 >> 4), idO, k > 0 ? 1u : more);
-        tc::mma_commit(&sh.pv_done[i]);
-    };
-    int piece = 0;
-    for (int n = 0;; ++n) {
-        if (!wait_for(sh, &sh.info_full[n % kTiles], (n / kTiles) & 1)) break;
-        const int flags = sh.tile[n % kTiles].flags;
-        if (flags & kEnd) break;
-        const int st = n & 1;
-        if (flags & kFirst) {
-            if (!wait_for(sh, &sh.q_full, piece & 1) || !wait_for(sh, &sh.full[0][st], (n >> 1) & 1)) break;
-            ++piece;
-            tc::tc_fence_after();
+    bool ok = true;
+    for (int n = 0, piece = 0; ok; ++piece) {
+        ok = waited(&sh.info_full[n % kSteps], (n / kSteps) & 1);
+        if (!ok || uniform(sh.step[n % kSteps].flags & kEnd)) break;
+        int ahead = 0;                     // steps of the piece whose scores are on their way
+        const int steps = uniform(sh.step[n % kSteps].left) + 1;
+        ok = waited(&sh.q_full[i], piece & 1);
+        // the scores run two steps ahead of the values
 #pragma unroll 1
-            for (int i = 0; i < 2; ++i) scores(i, st);
-            tc::mma_commit(&sh.empty[0][st]);
-        }
-        const int nx = n + 1, sx = nx & 1;
-        bool ok = true;
-#pragma unroll 1
-        for (int i = 0; i < 2 && ok; ++i) {
-            ok = (i == 1 || wait_for(sh, &sh.full[1][st], (n >> 1) & 1)) && wait_for(sh, &sh.p_full[i], n & 1);
-            if (!ok) break;
-            tc::tc_fence_after();
-            values(i, st, !(flags & kFirst));
-            if (i == 1) tc::mma_commit(&sh.empty[1][st]);
-            if (!(flags & kLast)) {
-                ok = i == 1 || wait_for(sh, &sh.full[0][sx], (nx >> 1) & 1);
+        for (int z = -2; z < steps && ok; ++z) {
+            if (z >= 0) {
+                const int m = n + z, bf = m % kBuffers;
+                ok = waited(&sh.full[1][bf], (m / kBuffers) & 1) && waited(&sh.p_full[i][m & 1], (m >> 1) & 1);
                 if (!ok) break;
                 tc::tc_fence_after();
-                scores(i, sx);
-                if (i == 1) tc::mma_commit(&sh.empty[0][sx]);
+                const uint64_t b = dV + bf * (kTileBytes >> 4);
+                const uint32_t more = z > 0 ? 1u : 0u;
+                if (leader) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc::mma_f16_ts(tO, tS + (m & 1) * kN + k * 8, b + k * (2048 >> 4), idO, k > 0 ? 1u : more);
+                    tc::mma_commit(&sh.pv_done[i][m & 1]);
+                    tc::mma_commit(&sh.empty[1][bf]);
+                }
+                __syncwarp();
             }
+            if (ahead < steps) ok = scores(n + ahead++);
         }
-        if (!ok) break;
-        tc::mbar_arrive(&sh.info_empty[n % kTiles]);
+        n += steps;
     }
     // every MMA has ended before tensor memory is given back
-    tc::mma_commit(&sh.drain);
-    tc::mbar_wait(&sh.drain, 0, clock64() + tc::kWaitCycles);
+    if (leader) tc::mma_commit(&sh.drain[i]);
+    __syncwarp();
+    tc::mbar_wait(&sh.drain[i], 0, clock64() + tc::kWaitCycles);
 }
 
 // =================== the walk ===============================================
@@ -617,7 +670,7 @@ __device__ __forceinline__ void walk_role(const AttnArgs& p, Shared& sh, uint8_t
     int n = 0;
     bool ok = true;
     while (ok && more) {
-        const bool begins = w.t0 == 0, ends = w.t1 == w.span.tiles;
+        const bool begins = w.t0 == 0, ends = w.t1 == w.span.steps;
         const int slot = begins && ends ? -1 : (int)blockIdx.x * 2 + (begins ? 1 : 0);
         if (lane == 0 && slot >= 0) {
             int* m = p.meta + blockIdx.x * kMeta;
@@ -643,10 +696,10 @@ __device__ __forceinline__ void walk_role(const AttnArgs& p, Shared& sh, uint8_t
         int page = -1;
         float sk = 0.f, lsv = 0.f, isv = 1.f;
         for (int i = w.t0; i < w.t1; ++i, ++n) {
-            const int in = (i - w.t0) & 15;
-            if (in == 0) {   // pages and scales of 16 tiles, a page per lane
-                const int j = i + (lane >> 1);
-                const int tok = w.span.tile_of(j) * kN + (lane & 1) * kPage;
+            const int in = (i - w.t0) & 31;
+            if (in == 0) {   // pages and scales of 32 steps, one per lane
+                const int j = i + lane;
+                const int tok = w.span.step_of(j) * kN;
                 page = j < w.t1 && tok < w.r.len ? __ldg(p.table + (int64_t)w.b * p.width + tok / kPage) : -1;
                 if (page >= p.pages) page = -1;
                 const int64_t at = (int64_t)max(page, 0) * p.kv_heads + w.h;
@@ -656,63 +709,56 @@ __device__ __forceinline__ void walk_role(const AttnArgs& p, Shared& sh, uint8_t
                 lsv = lg2(sv);
                 isv = __fdividef(1.f, sv);
             }
-            const int pg0 = __shfl_sync(0xffffffffu, page, 2 * in), pg1 = __shfl_sync(0xffffffffu, page, 2 * in + 1);
-            ok = wait_for(sh, &sh.info_empty[n % kTiles], ((n / kTiles) & 1) ^ 1);
-            ok = __all_sync(0xffffffffu, ok);
+            const int pg = __shfl_sync(0xffffffffu, page, in);
+            ok = __all_sync(0xffffffffu, wait_for(sh, &sh.info_empty[n % kSteps], ((n / kSteps) & 1) ^ 1));
             if (!ok) break;
-            Tile& ti = sh.tile[n % kTiles];
-            if ((lane >> 1) == in) {
-                ti.there[lane & 1] = page >= 0;
-                ti.sk[lane & 1] = sk;
-                ti.lsv[lane & 1] = lsv;
-                ti.isv[lane & 1] = isv;
-            }
-            if (lane == 0) {
-                ti.flags = (i == w.t0 ? kFirst : 0) | (i + 1 == w.t1 ? kLast : 0);
-                ti.key0 = w.span.tile_of(i) * kN;
-                ti.len = w.r.len;
-                ti.pre = w.r.pre;
-                ti.n = w.r.n;
-                ti.first = w.r.first;
-                ti.token0 = w.pair * 2 * p.tq;
-                ti.h = w.h;
-                ti.slot = slot;
+            if (lane == in) {
+                Step& st = sh.step[n % kSteps];
+                st.flags = i == w.t0 ? kFirst : 0;
+                st.key0 = w.span.step_of(i) * kN;
+                st.left = w.t1 - 1 - i;
+                st.there = page >= 0;
+                st.sk = sk;
+                st.lsv = lsv;
+                st.isv = isv;
+                st.len = w.r.len;
+                st.pre = w.r.pre;
+                st.n = w.r.n;
+                st.first = w.r.first;
+                st.token0 = w.pair * 2 * p.tq;
+                st.h = w.h;
+                st.slot = slot;
+                tc::mbar_arrive(&sh.info_full[n % kSteps]);
             }
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sh.info_full[n % kTiles]);
-            // codes, a page of one operand per copy
-            const uint32_t bytes = (pg0 >= 0 ? kCodeBytes / 2 : 0) + (pg1 >= 0 ? kCodeBytes / 2 : 0);
-            const int64_t a0 = ((int64_t)max(pg0, 0) * p.kv_heads + w.h) * (kCodeBytes / 2);
-            const int64_t a1 = ((int64_t)max(pg1, 0) * p.kv_heads + w.h) * (kCodeBytes / 2);
+            const int64_t at = ((int64_t)max(pg, 0) * p.kv_heads + w.h) * kCodeBytes;
 #pragma unroll 1
             for (int v = 0; v < 2; ++v) {   // K, then V
-                ok = __all_sync(0xffffffffu, wait_for(sh, &sh.c_empty[v], (n & 1) ^ 1));
-                if (!ok) {   // the K codes on their way land before the CTA ends
-                    if (v == 1) tc::mbar_wait(&sh.c_full[0], n & 1, clock64() + tc::kWaitCycles);
-                    break;
-                }
+                ok = __all_sync(0xffffffffu, wait_for(sh, &sh.c_empty[v][n & 1], ((n >> 1) & 1) ^ 1));
+                if (!ok) break;
                 if (lane == 0) {
-                    const uint8_t* src = v ? p.v : p.k;
-                    uint8_t* dst = sKc + v * kCodeBytes;
-                    tc::mbar_arrive_expect_tx(&sh.c_full[v], bytes);
-                    if (pg0 >= 0) tc::bulk_g2s(dst, src + a0, kCodeBytes / 2, &sh.c_full[v]);
-                    if (pg1 >= 0) tc::bulk_g2s(dst + kCodeBytes / 2, src + a1, kCodeBytes / 2, &sh.c_full[v]);
+                    uint64_t* bar = &sh.c_full[v][n & 1];
+                    tc::mbar_arrive_expect_tx(bar, pg >= 0 ? kCodeBytes : 0);
+                    if (pg >= 0) tc::bulk_g2s(sKc + (2 * v + (n & 1)) * kCodeBytes, (v ? p.v : p.k) + at, kCodeBytes, bar);
                 }
+                __syncwarp();
             }
             if (!ok) break;
         }
         if (ok) more = w.next(p);
     }
-    // the copies of the last tile have landed before the CTA ends, whatever
-    // became of their readers
-    if (n > 0) {
-        tc::mbar_wait(&sh.c_full[0], (n - 1) & 1, clock64() + tc::kWaitCycles);
-        tc::mbar_wait(&sh.c_full[1], (n - 1) & 1, clock64() + tc::kWaitCycles);
+    if (ok) {
+        ok = __all_sync(0xffffffffu, wait_for(sh, &sh.info_empty[n % kSteps], ((n / kSteps) & 1) ^ 1));
+        if (ok && lane == 0) {
+            sh.step[n % kSteps].flags = kEnd;
+            tc::mbar_arrive(&sh.info_full[n % kSteps]);
+        }
     }
-    if (!ok || !__all_sync(0xffffffffu, wait_for(sh, &sh.info_empty[n % kTiles], ((n / kTiles) & 1) ^ 1))) return;
-    if (lane == 0) {
-        sh.tile[n % kTiles].flags = kEnd;
-        tc::mbar_arrive(&sh.info_full[n % kTiles]);
+    if (!ok) {
+        // copies may be on their way to readers that have given up: they land
+        // within microseconds; the CTA ends long after
+        const long long until = clock64() + 20000000;
+        while (clock64() < until) __nanosleep(1000);
     }
 }
 
@@ -772,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
         const int first_b = b;
         for (int i = q0; i < q1; ++i) {
             while (i >= s_pairs[b + 1]) ++b;
-            mine += span_of(p, seen_of<kN>(p, b), i - s_pairs[b]).tiles + kPieceTiles;
+            mine += span_of(p, seen_of<kN>(p, b), i - s_pairs[b]).steps + kPieceSteps;
         }
         int64_t incl = mine;
 #pragma unroll
@@ -801,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
                 b = first_b;
                 for (;; ++i) {
                     while (i >= s_pairs[b + 1]) ++b;
-                    const int n = span_of(p, seen_of<kN>(p, b), i - s_pairs[b]).tiles + kPieceTiles;
+                    const int n = span_of(p, seen_of<kN>(p, b), i - s_pairs[b]).steps + kPieceSteps;
                     if (off < n) break;
                     off -= n;
                 }
@@ -816,25 +862,25 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
 
     // ---- barriers and tensor memory ---------------------------------------
     if (t == 0) {
-        for (int i = 0; i < kTiles; ++i) {
+        for (int i = 0; i < kSteps; ++i) {
             tc::mbar_init(&sh.info_full[i], 1);
-            tc::mbar_init(&sh.info_empty[i], kSoftmaxWarps + kCodeWarps + 1);
+            tc::mbar_init(&sh.info_empty[i], kSoftmaxWarps + kCodeWarps);
         }
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&sh.full[0][i], kCodeWarps);
-            tc::mbar_init(&sh.full[1][i], kCodeWarps);
-            tc::mbar_init(&sh.empty[0][i], 1);
-            tc::mbar_init(&sh.empty[1][i], 1);
-            tc::mbar_init(&sh.s_full[i], 1);
-            tc::mbar_init(&sh.p_full[i], kSoftmaxWarps / 2);
-            tc::mbar_init(&sh.pv_done[i], 1);
+            tc::mbar_init(&sh.q_full[i], kSoftmaxWarps / 2);
+            tc::mbar_init(&sh.drain[i], 1);
+            for (int z = 0; z < kBuffers; ++z) {
+                tc::mbar_init(&sh.full[i][z], kCodeWarps);
+                tc::mbar_init(&sh.empty[i][z], 2);
+            }
+            for (int z = 0; z < 2; ++z) {
+                tc::mbar_init(&sh.c_full[i][z], 1);
+                tc::mbar_init(&sh.c_empty[i][z], kCodeWarps);
+                tc::mbar_init(&sh.s_full[i][z], 1);
+                tc::mbar_init(&sh.pv_done[i][z], 1);
+                tc::mbar_init(&sh.p_full[i][z], kSoftmaxWarps / 2);
+            }
         }
-        tc::mbar_init(&sh.c_full[0], 1);
-        tc::mbar_init(&sh.c_full[1], 1);
-        tc::mbar_init(&sh.c_empty[0], kCodeWarps);
-        tc::mbar_init(&sh.c_empty[1], kCodeWarps);
-        tc::mbar_init(&sh.q_full, kSoftmaxWarps);
-        tc::mbar_init(&sh.drain, 1);
         sh.failed = 0;
         tc::fence_mbar_init();
     }
@@ -846,10 +892,9 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    uint8_t* sK = base;
-    uint8_t* sV = base + 2 * kTileBytes;
-    uint8_t* sQ = base + 4 * kTileBytes;
-    uint8_t* sKc = base + 6 * kTileBytes;
+    uint8_t* sK = base;                                   // K tiles, then V tiles
+    uint8_t* sQ = base + 2 * kBuffers * kTileBytes;
+    uint8_t* sKc = sQ + 2 * kQBytes;                      // K codes, then V codes
 
     if (warp < kSoftmaxWarps) {
         more_registers<kSoftmaxRegs>();
@@ -859,8 +904,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
         code_role<CODE>(sh, sK, sKc, t - 32 * kSoftmaxWarps, lane);
     } else {
         fewer_registers<kOtherRegs>();
-        if (warp == kMmaWarp) {
-            if (lane == 0) mma_role(sh, sK, sV, sQ, tmem);
+        if (warp == kMmaWarp || warp == kMmaWarp + 2) {
+            mma_role(sh, uniform(tc::smem_u32(sK)), uniform(tc::smem_u32(sQ)), uniform(tmem), uniform(warp - kMmaWarp) >> 1);
         } else if (warp == kWalkWarp) {
             walk_role(p, sh, sKc, start_h, left, lane);
         }
