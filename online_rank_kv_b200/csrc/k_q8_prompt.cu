@@ -83,6 +83,7 @@ struct Shared {
     // Even and odd steps apart: a softmax may be a step ahead of its values'
     // product, and a parity tells only neighbouring phases apart.
     uint64_t pv_done[2][2];
+    uint64_t turn[2][kSoftmaxWarps / 2];
     uint32_t tmem;
     int failed;
     int64_t scan[16];
@@ -416,6 +417,10 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
                 }
             }
             // ---- weights ----
+            // The two tiles' warps of a scheduler take turns at the exponentials:
+            // each then has them to itself and the other its remaining work.
+            ok = wait_for(sh, &sh.turn[i][warp & 3], i == 0 ? (n & 1) ^ 1 : n & 1);
+            if (!__all_sync(0xffffffffu, ok)) return;
             // One fused multiply-add per weight: x - M with x unrounded, M and
             // M - log2 s_v rounded, off by 2^-24 |M| between pages.  From
             // |M| = 2^10 on, x is rounded like M was first, so that the row's
@@ -445,6 +450,8 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
                 }
                 tc::tmem_st16(tSn + 16 * c, o);
             }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sh.turn[i ^ 1][warp & 3]);
             const float2 s2 = split(add2(sum0, sum1));
             l += (s2.x + s2.y) * st.isv;
             const int left = st.left;
@@ -867,6 +874,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
             tc::mbar_init(&sh.info_empty[i], kSoftmaxWarps + kCodeWarps);
         }
         for (int i = 0; i < 2; ++i) {
+            for (int z = 0; z < kSoftmaxWarps / 2; ++z) tc::mbar_init(&sh.turn[i][z], 1);
             tc::mbar_init(&sh.q_full[i], kSoftmaxWarps / 2);
             tc::mbar_init(&sh.drain[i], 1);
             for (int z = 0; z < kBuffers; ++z) {
