@@ -60,8 +60,8 @@ int sm_count() {
 // queries of one KV head fit it, else two (which halves the passes over K, V).
 int row_tiles8(int g, int max_new) { return (int64_t)max_new * g <= 8 ? 1 : 2; }
 
-int64_t rows_floats(int ctas, int tiles8) {
-    return (int64_t)ctas * q8::kPartsPerCta * 8 * tiles8 * (kHeadDim + 2);
+int64_t rows_floats(int ctas, int tiles8, int dtype) {
+    return (int64_t)ctas * q8::rows_parts(tiles8, dtype == ISKV_F32) * 8 * tiles8 * (kHeadDim + 2);
 }
 
 int64_t prompt_floats(int ctas) { return (int64_t)ctas * 2 * q8::kPromptRows * (kHeadDim + 2); }
@@ -136,7 +136,7 @@ int64_t iskv_q8_workspace(int32_t q_heads, int32_t kv_heads, int64_t tokens, int
     const int ctas = sm_count();
     const int g = q_heads / kv_heads;
     if (is_prompt(g, max_new, dtype)) return prompt_floats(ctas) * 4 + (int64_t)ctas * q8::kMetaBytes;
-    return rows_floats(ctas, row_tiles8(g, max_new)) * 4 + (int64_t)ctas * q8::kMetaBytes;
+    return rows_floats(ctas, row_tiles8(g, max_new), dtype) * 4 + (int64_t)ctas * q8::kMetaBytes;
 }
 
 int iskv_q8_attention(const iskv_q8_pages* store, const iskv_q8_attention_args* a, void* stream) {
@@ -190,7 +190,7 @@ int iskv_q8_attention(const iskv_q8_pages* store, const iskv_q8_attention_args* 
     const bool prompt = is_prompt(g, a->max_new, a->dtype);
     p.tq = (prompt ? q8::kPromptRows / 2 : 8 * tiles8) / g;
     p.ctas = sm_count();
-    const int64_t parts = (int64_t)p.ctas * (prompt ? 2 * q8::kPromptRows : q8::kPartsPerCta * 8 * tiles8);
+    const int64_t parts = (int64_t)p.ctas * (prompt ? 2 * q8::kPromptRows : q8::rows_parts(tiles8, a->dtype == ISKV_F32) * 8 * tiles8);
     p.part = static_cast<float*>(a->workspace);
     p.ml = p.part + parts * kHeadDim;
     p.meta = reinterpret_cast<int*>(p.ml + parts * 2);

@@ -39,14 +39,22 @@ namespace q8 {
 
 namespace {
 
-constexpr int kWarps = kRowWarps;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 3;
+// Warps and pipeline stages per warp.  The loop is bound by the latency of its
+// own instructions, so the light variant takes 12 warps of 168 registers with
+// two stages each (measured against 8 warps with three: 8 x 32K tokens 117 ->
+// __ us); two row tiles or fp32 parts need more registers and take 8.
+template <int NT, bool F32>
+struct Shape {
+    static constexpr int kWarps = rows_warps(NT, F32);
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kStages = kWarps > 8 ? 2 : 3;
+};
 constexpr int kStoreBytes = kStepTokens * kHeadDim;      // K or V of one step: 4 KB
 constexpr int kStageBytes = 2 * kStoreBytes;
-constexpr int kSmemBytes = kWarps * kStages * kStageBytes;
 
 using Req = Seen<kStepTokens>;
+
+__device__ __forceinline__ int tiles_of(const AttnArgs& p, int n) { return (n + p.tq - 1) / p.tq; }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -79,27 +87,26 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
     return v;
 }
 
-// A place in the numbered-through steps.
+// A place in the numbered-through steps.  (No divisions on the way: straight-line
+// code is fetched from L2 by every SM at every launch, and a call of this kernel
+// is as long as its code is.)
 struct Cursor {
-    int b, item, step;    // request, head * tiles + tile, step
+    int b, h, tile, step;
     int tiles;
     Req r;
     __device__ __forceinline__ void load(const AttnArgs& p) {
         r = seen_of<kStepTokens>(p, b);
-        tiles = (r.n + p.tq - 1) / p.tq;
-    }
-    __device__ __forceinline__ void start(const AttnArgs& p, int b_, int64_t off) {
-        b = b_;
-        load(p);
-        item = (int)(off / r.steps);
-        step = (int)(off % r.steps);
+        tiles = tiles_of(p, r.n);
     }
     // to the next step; the caller knows that there is one
     __device__ __forceinline__ void next(const AttnArgs& p) {
         if (++step < r.steps) return;
         step = 0;
-        if (++item < tiles * p.kv_heads) return;
-        item = 0;
+        if (++tile < tiles) return;
+        tile = 0;
+        if (++h < p.kv_heads) return;
+        h = 0;
+#pragma unroll 1
         do {
             ++b;
             load(p);
@@ -115,27 +122,19 @@ struct Part {
 
 __device__ __forceinline__ int64_t units_of(const AttnArgs& p, int b) {
     const Req r = seen_of<kStepTokens>(p, b);
-    return (int64_t)((r.n + p.tq - 1) / p.tq) * r.steps * p.kv_heads;
+    return (int64_t)tiles_of(p, r.n) * r.steps * p.kv_heads;
 }
 
-// Row n of an item: its query token and head, or false.
-__device__ __forceinline__ bool row_of(const AttnArgs& p, const Req& r, int item, int tiles, int n, int* token, int* head) {
-    const int h = item / tiles, tile = item % tiles;
-    const int k = n / p.g;
-    *token = tile * p.tq + k;
-    *head = h * p.g + n % p.g;
-    return k < p.tq && *token < r.n;
-}
-
-template <bool F32>
-__device__ __forceinline__ void store_out(const AttnArgs& p, int64_t at, const float* v, int n) {
-    // n consecutive elements (a multiple of 4)
+template <bool F32, int N>
+__device__ __forceinline__ void store_out(const AttnArgs& p, int64_t at, const float (&v)[N]) {
     if (F32) {
         float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
-        for (int i = 0; i < n / 4; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     } else {
         uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at);
-        for (int i = 0; i < n / 4; ++i) {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
             const __nv_bfloat162 a = __floats2bfloat162_rn(v[4 * i], v[4 * i + 1]);
             const __nv_bfloat162 b = __floats2bfloat162_rn(v[4 * i + 2], v[4 * i + 3]);
             o[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
@@ -148,12 +147,14 @@ __device__ __forceinline__ void store_out(const AttnArgs& p, int64_t at, const f
 template <int R, bool F32, typename At>
 __device__ __forceinline__ void join(const AttnArgs& p, int n, At at, int to, int b, int item) {
     const Req r = seen_of<kStepTokens>(p, b);
-    const int tiles = (r.n + p.tq - 1) / p.tq;
+    const int tiles = tiles_of(p, r.n), h = item / tiles, tile = item % tiles;
+#pragma unroll 1
     for (int e = threadIdx.x; e < R * 32; e += blockDim.x) {
-        const int row = e >> 5, d = (e & 31) * 4;
-        int token, head;
-        if (!row_of(p, r, item, tiles, row, &token, &head)) continue;
+        const int row = e >> 5, d = (e & 31) * 4, k = row / p.g;
+        const int token = tile * p.tq + k, head = h * p.g + row - k * p.g;
+        if (k >= p.tq || token >= r.n) continue;
         float M = -INFINITY;
+#pragma unroll 4
         for (int i = 0; i < n; ++i) M = fmaxf(M, p.ml[((int64_t)at(i) * R + row) * 2]);
         const float base = M == -INFINITY ? 0.f : M;
         float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
@@ -170,10 +171,10 @@ __device__ __forceinline__ void join(const AttnArgs& p, int n, At at, int to, in
             o[3] += w * v.w;
         }
         if (to < 0) {
-            const float inv = l > 0.f ? __fdiv_rn(1.f, l) : (l == 0.f ? 0.f : l);
+            const float inv = l > 0.f ? __fdividef(1.f, l) : (l == 0.f ? 0.f : l);
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] *= inv;
-            store_out<F32>(p, ((int64_t)(r.first + token) * p.kv_heads * p.g + head) * kHeadDim + d, o, 4);
+            store_out<F32, 4>(p, ((int64_t)(r.first + token) * p.kv_heads * p.g + head) * kHeadDim + d, o);
         } else {
             const int64_t k = (int64_t)to * R + row;
             *reinterpret_cast<float4*>(p.part + k * kHeadDim + d) = make_float4(o[0], o[1], o[2], o[3]);
@@ -188,7 +189,9 @@ __device__ __forceinline__ void join(const AttnArgs& p, int n, At at, int to, in
 constexpr int kMeta = 4;
 
 template <int CODE, int NT, bool F32, bool MOD>
-__global__ void __launch_bounds__(kThreads, 1) q8_rows_kernel(const AttnArgs p) {
+__global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(const AttnArgs p) {
+    constexpr int kWarps = Shape<NT, F32>::kWarps, kThreads = Shape<NT, F32>::kThreads, kStages = Shape<NT, F32>::kStages;
+    constexpr int kPartsPerCta = 2 * kWarps + 2;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t s_scan[kWarps], s_off[kWarps];
     __shared__ int s_b[kWarps];
@@ -203,6 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_rows_kernel(const AttnArgs p) 
     const int chunk = (p.batch + kThreads - 1) / kThreads;
     const int b0 = min(p.batch, t * chunk), b1 = min(p.batch, b0 + chunk);
     int64_t mine = 0;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) mine += units_of(p, b);
     int64_t incl = mine;
 #pragma unroll
@@ -227,12 +231,13 @@ __global__ void __launch_bounds__(kThreads, 1) q8_rows_kernel(const AttnArgs p) 
     }
     const int64_t per_warp = (u1 - u0 + kWarps - 1) / kWarps;
     if (mine > 0) {
-#pragma unroll
+#pragma unroll 1
         for (int w = 0; w < kWarps; ++w) {
             const int64_t u = u0 + w * per_warp;
             if (u < u1 && u >= ex && u < ex + mine) {
                 int64_t off = u - ex;
                 int b = b0;
+#pragma unroll 1
                 for (;; ++b) {
                     const int64_t n = units_of(p, b);
                     if (off < n) break;
@@ -246,157 +251,165 @@ __global__ void __launch_bounds__(kThreads, 1) q8_rows_kernel(const AttnArgs p) 
     __syncthreads();
 
     const int64_t w0 = u0 + warp * per_warp;
-    const int64_t left = min(u1, w0 + per_warp) - w0;   // steps of this warp (may be <= 0)
+    const int64_t n_steps = min(u1, w0 + per_warp) - w0;   // steps of this warp (may be <= 0)
     uint8_t* ring = smem + warp * (kStages * kStageBytes);
     const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
     const int my_parts = (cta * kPartsPerCta) + 2 * warp;
+    // rows of this lane inside a row tile, as (token, head of the group): of its
+    // query row r and of its result rows 2q, 2q + 1 (8 more per tile of 8)
+    int q_k[NT], q_g[NT], o_k[NT][2], o_g[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        q_k[n] = (n * 8 + r) / p.g;
+        q_g[n] = n * 8 + r - q_k[n] * p.g;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int src = 8 * q + 4 * c;
+            o_k[n][c] = __shfl_sync(0xffffffffu, q_k[n], src);
+            o_g[n][c] = __shfl_sync(0xffffffffu, q_g[n], src);
+        }
+    }
 
-    if (left > 0) {
+    if (n_steps > 0) {
         Cursor in, at;
-        in.start(p, s_b[warp], s_off[warp]);
-        at = in;
+        at.b = s_b[warp];
+        at.load(p);
+        {
+            int64_t off = s_off[warp];
+            const int64_t per_head = (int64_t)at.tiles * at.r.steps;
+            at.h = (int)(off / per_head);
+            const int rest = (int)(off - at.h * per_head);
+            at.tile = rest / at.r.steps;
+            at.step = rest - at.tile * at.r.steps;
+        }
+        in = at;
+        int left = (int)min(n_steps, (int64_t)INT32_MAX), to_issue = left;
 
-        // ---- loads: step i of this warp into stage i % kStages ------------
+        uint32_t qf[PARTS][NT][8][2];          // queries as B fragments
+        float rowf[NT][2];                     // score factor of rows 2q, 2q + 1 of each tile of 8
+        int pos[NT][2], see_from[NT][2];       // the causal span (see_from, pos]
+        float slope[NT][2];
+        float M[NT][2], l[NT][2], o[NT][8][4];
+        int pmin = 0, pmax = 0, first_step = 0;
+        bool fresh = true;
+
         auto page_of = [&](const Cursor& c) {
             const int tok = c.r.step_of(c.step) * kStepTokens;
             return tok < c.r.len ? p.table[(int64_t)c.b * p.width + tok / kPage] : -1;
         };
-        auto issue = [&](const Cursor& c, int page, int stage) {
-            const int tok = c.r.step_of(c.step) * kStepTokens;
-            const int h = c.item / c.tiles;
-            const bool ok = page >= 0 && page < p.pages;
-            const int rows = ok ? c.r.len - tok : 0;   // rows of the step that are stored
-            const int64_t base = ((int64_t)(ok ? page : 0) * p.kv_heads + h) * (kPage * kHeadDim) +
-                                 (tok % kPage) * kHeadDim;
-            const int ch = lane & 7, row = lane >> 3;
-            const uint32_t dst = ring_at + stage * kStageBytes;
+        int page = page_of(in), fill = 0, stage = 0;
+        // kStages - 1 steps are on their way before the first is used
+#pragma unroll 1
+        for (int ahead = 1 - kStages; left > 0; ++ahead) {
+            if (to_issue > 0) {
+                const int tok = in.r.step_of(in.step) * kStepTokens;
+                const bool ok = page >= 0 && page < p.pages;
+                const int rows = ok ? in.r.len - tok : 0;   // rows of the step that are stored
+                const int ch = lane & 7, row = lane >> 3;
+                const int64_t src = ((int64_t)(ok ? page : 0) * p.kv_heads + in.h) * (kPage * kHeadDim) +
+                                    ((tok % kPage) + row) * kHeadDim + ch * 16;
+                const uint8_t* sk8 = p.k + src;
+                const uint8_t* sv8 = p.v + src;
+                const uint32_t dst = ring_at + fill * kStageBytes + row * kHeadDim;
+                const uint32_t d0 = dst + ((ch ^ row) << 4), d1 = dst + ((ch ^ (row + 4)) << 4);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int rr = row + 4 * i;
-                const uint32_t d = dst + rr * kHeadDim + ((ch ^ (rr & 7)) << 4);
-                const int64_t s = base + rr * kHeadDim + ch * 16;
-                const uint32_t bytes = rr < rows ? 16u : 0u;   // rows behind the end read as zeros
-                cp16(d, p.k + s, bytes);
-                cp16(d + kStoreBytes, p.v + s, bytes);
-            }
-            if (lane == 0) s_page[warp][stage] = ok ? page : -1;
-        };
-        int64_t issued = 0;
-        int page = page_of(in);
-#pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) {
-            if (issued < left) {
-                issue(in, page, s);
-                if (++issued < left) {
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t d = ((i & 1) ? d1 : d0) + i * 4 * kHeadDim;
+                    const uint32_t bytes = row + 4 * i < rows ? 16u : 0u;   // rows behind the end read as zeros
+                    cp16(d, sk8 + i * 4 * kHeadDim, bytes);
+                    cp16(d + kStoreBytes, sv8 + i * 4 * kHeadDim, bytes);
+                }
+                if (lane == 0) s_page[warp][fill] = ok ? page : -1;
+                fill = fill + 1 == kStages ? 0 : fill + 1;
+                if (--to_issue > 0) {
                     in.next(p);
                     page = page_of(in);
                 }
             }
             cp_commit();
-        }
+            if (ahead < 0) continue;
 
-        uint32_t qf[PARTS][NT][8][2];          // queries as B fragments
-        float rowf[NT][2];                     // score factor of rows 2q, 2q + 1 of each tile of 8
-        int pos[NT][2], seen_to[NT][2], seen_from[NT][2];   // the causal span (seen_from, seen_to]
-        float slope[NT][2];
-        float M[NT][2], l[NT][2], o[NT][8][4];
-        int pmin = 0, pmax = 0;
-
-        auto begin = [&]() {   // of an item: its queries
-            int token, head;
+            if (fresh) {   // an item begins: its queries
+                fresh = false;
+                first_step = at.step;
+                pmin = at.r.len - at.r.n + at.tile * p.tq;
+                pmax = min(at.r.len - 1, pmin + p.tq - 1);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float x[32];
-                const bool on = row_of(p, at.r, at.item, at.tiles, n * 8 + r, &token, &head);
-                const int64_t src = (int64_t)(at.r.first + token) * p.q_stride + head * kHeadDim + 32 * q;
-                if (F32) {
-                    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + src);
+                for (int n = 0; n < NT; ++n) {
+                    float x[32];
+                    const int token = at.tile * p.tq + q_k[n];
+                    const bool on = q_k[n] < p.tq && token < at.r.n;
+                    const int64_t src = (int64_t)(at.r.first + token) * p.q_stride + (at.h * p.g + q_g[n]) * kHeadDim + 32 * q;
+                    if (F32) {
+                        const float4* f4 = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + src);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 v = on ? __ldg(s + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-                        x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
-                    }
-                } else {
-                    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + src);
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 v = on ? __ldg(f4 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                            x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+                        }
+                    } else {
+                        const uint4* u4 = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + src);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint4 v = on ? __ldg(s + i) : make_uint4(0u, 0u, 0u, 0u);
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 v = on ? __ldg(u4 + i) : make_uint4(0u, 0u, 0u, 0u);
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            x[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
-                            x[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+                            for (int k = 0; k < 4; ++k) {
+                                x[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
+                                x[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+                            }
                         }
                     }
-                }
-                float top = 0.f;
+                    float top = 0.f;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(x[i]));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // 2^up brings the row's largest element into [2^14, 2^15)
-                int up = 14 - ((int)(__float_as_uint(top) >> 23) - 127);
-                up = max(-126, min(126, up));
-                const float f = __uint_as_float((uint32_t)(up + 127) << 23);
-                const float down = __uint_as_float((uint32_t)(127 - up) << 23) * (p.scale * (MOD ? 1.f : kLog2e));
+                    for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(x[i]));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    // 2^up brings the row's largest element into [2^14, 2^15)
+                    int up = 14 - ((int)(__float_as_uint(top) >> 23) - 127);
+                    up = max(-126, min(126, up));
+                    const float f = __uint_as_float((uint32_t)(up + 127) << 23);
+                    const float down = __uint_as_float((uint32_t)(127 - up) << 23) * (p.scale * (MOD ? 1.f : kLog2e));
 #pragma unroll
-                for (int s = 0; s < 8; ++s) {
+                    for (int s = 0; s < 8; ++s) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float a = x[4 * s + 2 * i] * f, b = x[4 * s + 2 * i + 1] * f;
-                        qf[0][n][s][i] = pack(a, b);
-                        if (F32) {
-                            const float2 hi = unpack(qf[0][n][s][i]);
-                            qf[PARTS - 1][n][s][i] = pack(a - hi.x, b - hi.y);
+                        for (int i = 0; i < 2; ++i) {
+                            const float a = x[4 * s + 2 * i] * f, b = x[4 * s + 2 * i + 1] * f;
+                            qf[0][n][s][i] = pack(a, b);
+                            if (F32) {
+                                const float2 hi = unpack(qf[0][n][s][i]);
+                                qf[PARTS - 1][n][s][i] = pack(a - hi.x, b - hi.y);
+                            }
                         }
                     }
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        rowf[n][c] = __shfl_sync(0xffffffffu, down, 8 * q + 4 * c);
+                        const int tk = at.tile * p.tq + o_k[n][c];
+                        pos[n][c] = at.r.len - at.r.n + min(tk, at.r.n - 1);
+                        slope[n][c] = MOD && p.slopes && o_k[n][c] < p.tq ? p.slopes[at.h * p.g + o_g[n][c]] * kLog2e : 0.f;
+                        see_from[n][c] = p.window > 0 ? max(-1, pos[n][c] - p.window) : -1;
+                        M[n][c] = -INFINITY;
+                        l[n][c] = 0.f;
+                    }
+#pragma unroll
+                    for (int m = 0; m < 8; ++m)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[n][m][i] = 0.f;
                 }
-                rowf[n][0] = __shfl_sync(0xffffffffu, down, 8 * q);
-                rowf[n][1] = __shfl_sync(0xffffffffu, down, 8 * q + 4);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const bool there = row_of(p, at.r, at.item, at.tiles, n * 8 + 2 * q + i, &token, &head);
-                    pos[n][i] = at.r.len - at.r.n + min(token, at.r.n - 1);
-                    slope[n][i] = MOD && p.slopes && there ? p.slopes[head] * kLog2e : 0.f;
-                    seen_to[n][i] = pos[n][i];
-                    seen_from[n][i] = p.window > 0 ? max(-1, pos[n][i] - p.window) : -1;
-                    M[n][i] = -INFINITY;
-                    l[n][i] = 0.f;
-                }
-#pragma unroll
-                for (int m = 0; m < 8; ++m)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[n][m][i] = 0.f;
             }
-            const int tile = at.item % at.tiles;
-            pmin = at.r.len - at.r.n + tile * p.tq;
-            pmax = min(at.r.len - 1, pmin + p.tq - 1);
-        };
 
-        int first_step = at.step;
-        begin();
-        for (int64_t i = 0; i < left; ++i) {
-            // keep kStages - 1 steps in flight
-            if (issued < left) {
-                issue(in, page, (int)(issued % kStages));
-                if (++issued < left) {
-                    in.next(p);
-                    page = page_of(in);
-                }
-            }
-            cp_commit();
             cp_wait<kStages - 1>();
             __syncwarp();
-            const int stage = (int)(i % kStages);
             const int this_page = s_page[warp][stage];
             const int tok = at.r.step_of(at.step) * kStepTokens;
             const int stop = this_page < 0 ? 0 : at.r.len;      // stored tokens end here
-            const int h = at.item / at.tiles;
-            const int64_t block = (int64_t)max(this_page, 0) * p.kv_heads + h;
+            const int64_t block = (int64_t)max(this_page, 0) * p.kv_heads + at.h;
             const float sk = __ldg(p.k_scale + block);
             float sv = __ldg(p.v_scale + block);
             sv = sv > 0.f ? sv : 1.f;                             // a block of zeros
             const uint32_t kb = ring_at + stage * kStageBytes, vb = kb + kStoreBytes;
+            stage = stage + 1 == kStages ? 0 : stage + 1;
 
             // ---- S^T = K Q^T: two tiles of 16 tokens ----------------------
             float sc[NT][2][4];
@@ -450,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_rows_kernel(const AttnArgs p) 
                         }
                         x += lsv;
                         if (!whole) {
-                            const bool on = key < stop && ((key <= seen_to[n][c] && key > seen_from[n][c]) || key < at.r.pre);
+                            const bool on = key < stop && ((key <= pos[n][c] && key > see_from[n][c]) || key < at.r.pre);
                             x = on ? x : -INFINITY;
                         }
                         sc[n][m][e] = x;
@@ -535,28 +548,21 @@ __global__ void __launch_bounds__(kThreads, 1) q8_rows_kernel(const AttnArgs p) 
             __syncwarp();   // the stage may be filled again
 
             // ---- end of an item, or of this warp's share -------------------
+            --left;
             const bool last = at.step + 1 == at.r.steps;
-            if (last || i + 1 == left) {
+            if (last || left == 0) {
                 const bool whole_item = last && first_step == 0;
-                const int slot = s_part[warp][0].id < 0 && first_step != 0 ? 0 : 1;
-                float den[NT][2];
+                const int slot = first_step != 0 ? 0 : 1;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        float s = l[n][c];
-                        s += __shfl_xor_sync(0xffffffffu, s, 4);
-                        s += __shfl_xor_sync(0xffffffffu, s, 8);
-                        s += __shfl_xor_sync(0xffffffffu, s, 16);
-                        den[n][c] = s;
-                    }
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        int token, head;
-                        const int row = n * 8 + 2 * q + c;
-                        if (!row_of(p, at.r, at.item, at.tiles, row, &token, &head)) continue;
+                        float den = l[n][c];
+                        den += __shfl_xor_sync(0xffffffffu, den, 4);
+                        den += __shfl_xor_sync(0xffffffffu, den, 8);
+                        den += __shfl_xor_sync(0xffffffffu, den, 16);
+                        const int token = at.tile * p.tq + o_k[n][c], head = at.h * p.g + o_g[n][c];
+                        if (o_k[n][c] >= p.tq || token >= at.r.n) continue;
                         float v[16];
 #pragma unroll
                         for (int m = 0; m < 8; ++m) {
@@ -564,31 +570,24 @@ __global__ void __launch_bounds__(kThreads, 1) q8_rows_kernel(const AttnArgs p) 
                             v[2 * m + 1] = o[n][m][c + 2];
                         }
                         if (whole_item) {
-                            const float d = den[n][c];
-                            const float inv = d > 0.f ? __fdiv_rn(1.f, d) : (d == 0.f ? 0.f : d);
+                            const float inv = den > 0.f ? __fdividef(1.f, den) : (den == 0.f ? 0.f : den);
 #pragma unroll
                             for (int k = 0; k < 16; ++k) v[k] *= inv;
-                            store_out<F32>(p, ((int64_t)(at.r.first + token) * p.kv_heads * p.g + head) * kHeadDim + 16 * r, v, 16);
+                            store_out<F32, 16>(p, ((int64_t)(at.r.first + token) * p.kv_heads * p.g + head) * kHeadDim + 16 * r, v);
                         } else {
-                            const int64_t k = (int64_t)(my_parts + slot) * R + row;
+                            const int64_t k = (int64_t)(my_parts + slot) * R + n * 8 + 2 * q + c;
                             float4* to = reinterpret_cast<float4*>(p.part + k * kHeadDim + 16 * r);
 #pragma unroll
                             for (int m = 0; m < 4; ++m)
                                 to[m] = make_float4(v[4 * m], v[4 * m + 1], v[4 * m + 2], v[4 * m + 3]);
-                            if (r == 0) *reinterpret_cast<float2*>(p.ml + k * 2) = make_float2(M[n][c], den[n][c]);
+                            if (r == 0) *reinterpret_cast<float2*>(p.ml + k * 2) = make_float2(M[n][c], den);
                         }
                     }
                 if (!whole_item && lane == 0)
-                    s_part[warp][slot] = Part{((int64_t)at.b << 32) | (uint32_t)at.item, first_step == 0, last};
-                __syncwarp();
-                if (i + 1 < left) {
-                    at.next(p);
-                    first_step = 0;
-                    begin();
-                }
-            } else {
-                ++at.step;
+                    s_part[warp][slot] = Part{((int64_t)at.b << 32) | (uint32_t)(at.h * at.tiles + at.tile), first_step == 0, last};
+                fresh = true;
             }
+            if (left > 0) at.next(p);
         }
         cp_wait<0>();
     }
@@ -598,6 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_rows_kernel(const AttnArgs p) 
     if (t < kMeta) p.meta[cta * kMeta + t] = 0;
     __syncthreads();
     int i = 0;
+#pragma unroll 1
     while (i < 2 * kWarps) {
         const Part a = s_part[i >> 1][i & 1];
         if (a.id < 0) {
@@ -605,6 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_rows_kernel(const AttnArgs p) 
             continue;
         }
         int list[2 * kWarps], n = 0, end = i, ends = 0;
+#pragma unroll 1
         while (end < 2 * kWarps) {
             const Part z = s_part[end >> 1][end & 1];
             if (z.id >= 0) {
@@ -635,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_rows_kernel(const AttnArgs p) 
 // with the partials 0 of the CTAs after it, up to the one that ends it.
 template <int NT, bool F32>
 __global__ void __launch_bounds__(256) q8_join_kernel(const AttnArgs p) {
-    constexpr int R = 8 * NT;
+    constexpr int R = 8 * NT, kWarps = Shape<NT, F32>::kWarps, kPartsPerCta = 2 * kWarps + 2;
     const int cta = blockIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int* m = p.meta + cta * kMeta;
@@ -662,10 +663,12 @@ __global__ void __launch_bounds__(256) q8_join_kernel(const AttnArgs p) {
 
 template <int CODE, int NT, bool F32, bool MOD>
 cudaError_t run(const AttnArgs& a, cudaStream_t s) {
+    using S = Shape<NT, F32>;
+    constexpr int kSmemBytes = S::kWarps * S::kStages * kStageBytes;
     static SmemOnce once;
     cudaError_t e = once.set(q8_rows_kernel<CODE, NT, F32, MOD>, kSmemBytes);
     if (e != cudaSuccess) return e;
-    q8_rows_kernel<CODE, NT, F32, MOD><<<a.ctas, kThreads, kSmemBytes, s>>>(a);
+    q8_rows_kernel<CODE, NT, F32, MOD><<<a.ctas, S::kThreads, kSmemBytes, s>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

@@ -174,10 +174,10 @@ cudaError_t launch_q8_append(const AppendArgs& a, int code, int dtype, cudaStrea
 cudaError_t launch_q8_prompt(const AttnArgs& a, int code, cudaStream_t s);
 cudaError_t launch_q8_rows(const AttnArgs& a, int code, bool f32, int tiles8, cudaStream_t s);
 
-// floats of workspace of the split kernel for `ctas` CTAs and row tiles of
-// 8 * tiles8 rows: per CTA two partials of every warp and two of its own
-constexpr int kRowWarps = 8;
-constexpr int kPartsPerCta = 2 * kRowWarps + 2;
+// Warps per CTA of the split kernel for row tiles of 8 * tiles8 rows; its
+// workspace holds two partials of every warp and two of the CTA.
+constexpr int rows_warps(int tiles8, bool f32) { return tiles8 == 1 && !f32 ? 12 : 8; }
+constexpr int rows_parts(int tiles8, bool f32) { return 2 * rows_warps(tiles8, f32) + 2; }
 
 constexpr int kPromptRows = 256;   // query rows that the prompt kernel takes together
 constexpr int kMetaBytes = 32;     // per CTA, either kernel
