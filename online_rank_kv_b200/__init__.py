@@ -359,26 +359,34 @@ _DT_CODE = {d: c for c, d in _CODE_DT.items()}
 _DT_ELEM = {d: e for e, d in _TORCH_DT.items()}
 
 
-def _launch(device: torch.device, fn, where: str, *args, stream=None) -> None:
-    """Call a library function that takes the stream last, on `device`."""
-    if device.index != torch.cuda.current_device():
+def _raw_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# the same without building a stream object, where torch offers it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
+def _launch(device: int, fn, where: str, *args, stream=None) -> None:
+    """Call a library function that takes the stream last, on CUDA device `device`."""
+    if device != torch.cuda.current_device():
         with torch.cuda.device(device):
             return _launch(device, fn, where, *args, stream=stream)
-    code = fn(*args, _stream(stream))
+    code = fn(*args, _raw_stream(device) if stream is None else stream.cuda_stream)
     if code != OK:
         raise IskvError(code, where)
 
 
-def _int32(device, shape, t, name):
-    if t.dtype != torch.int32 or t.device != device or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
+def _int32(device: int, shape, t: torch.Tensor, name: str) -> int:
+    if t.dtype is not torch.int32 or t.get_device() != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on cuda:{device}")
     return t.data_ptr()
 
 
-def _on_cuda(t: torch.Tensor, name: str) -> torch.device:
+def _on_cuda(t: torch.Tensor, name: str) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    return t.device
+    return t.get_device()
 
 
 @dataclass
@@ -416,7 +424,7 @@ def page_plan(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, free: 
     if out is None:
         if tokens is None:
             raise ValueError("tokens (the number of slots) or out is needed")
-        out = PagePlan.empty(batch, tokens, dev)
+        out = PagePlan.empty(batch, tokens, lens.device)
     n = out.slots.shape[0]
     one = (1,)
     args = _PlanArgs(batch, width, free.shape[0], n, _int32(dev, (batch,), lens, "lens"),
@@ -459,23 +467,27 @@ class Q8Pages:
             raise ValueError(f"k and v must be [pages, kv_heads, {PAGE}, 128]")
         for t, shape, dt in ((v, k.shape, k.dtype), (k_scale, k.shape[:2], torch.float32),
                              (v_scale, k.shape[:2], torch.float32)):
-            if t.shape != shape or t.dtype != dt or t.device != dev:
+            if t.shape != shape or t.dtype != dt or t.get_device() != dev:
                 raise ValueError("v, k_scale and v_scale must match k in shape, device and type")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.device, self.kv_heads = dev, k.shape[1]
-        self._status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.device, self.kv_heads, self._dev = k.device, k.shape[1], dev
+        self._status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self._need = {}   # workspace bytes by (q_heads, max_new, type)
         self._c = _Q8Pages(k.shape[0], k.shape[1], 128, PAGE, _DT_CODE[k.dtype], _ptr(k), _ptr(v), _ptr(k_scale),
                            _ptr(v_scale))
+        self._ref, self._status_at = ctypes.byref(self._c), self._status.data_ptr()
 
     def _rows(self, t: torch.Tensor, heads: int | None, name: str) -> int:
-        if t.dim() != 3 or t.shape[2] != 128 or (heads is not None and t.shape[1] != heads) \
-                or (t.shape[0] > 0 and t.stride()[1:] != (128, 1)):
+        shape = t.shape
+        if len(shape) != 3 or shape[2] != 128 or (heads is not None and shape[1] != heads) \
+                or (shape[0] > 0 and t.stride()[1:] != (128, 1)):
             raise ValueError(f"{name} must be [tokens, heads, 128] with contiguous tokens")
-        if t.device != self.device:
+        if t.get_device() != self._dev:
             raise ValueError(f"{name} must be on {self.device}")
-        if t.dtype not in _DT_ELEM:
+        code = _DT_ELEM.get(t.dtype)
+        if code is None:
             raise TypeError(f"{name} must be bfloat16 or float32")
-        return _DT_ELEM[t.dtype]
+        return code
 
     def append(self, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
         """Store rows k, v [n, kv_heads, 128] (any token stride) in the slots
@@ -484,9 +496,8 @@ class Q8Pages:
         if self._rows(v, self.kv_heads, "v") != dt or v.shape != k.shape:
             raise ValueError("k and v must agree in shape and type")
         n = k.shape[0]
-        _launch(self.device, LIB.iskv_q8_append, "iskv_q8_append", ctypes.byref(self._c), k.data_ptr(), v.data_ptr(),
-                dt, k.stride(0), v.stride(0), n, _int32(self.device, (n,), slots, "slots"), self._status.data_ptr(),
-                stream=stream)
+        _launch(self._dev, LIB.iskv_q8_append, "iskv_q8_append", self._ref, k.data_ptr(), v.data_ptr(), dt, k.stride(0),
+                v.stride(0), n, _int32(self._dev, (n,), slots, "slots"), self._status_at, stream=stream)
 
     def attention(self, q: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, cu: torch.Tensor, max_new: int,
                   scale: float = 128 ** -0.5, cap: float = 0.0, slopes: torch.Tensor | None = None,
@@ -501,30 +512,34 @@ class Q8Pages:
         out [tokens, q_heads, 128] in q's type."""
         dt = self._rows(q, None, "q")
         n, heads = q.shape[0], q.shape[1]
-        dev = self.device
+        dev = self._dev
         if q.requires_grad and torch.is_grad_enabled():
             raise ValueError("attention over 8-bit pages is forward only: detach q")
         if out is None:
-            out = torch.empty(n, heads, 128, dtype=q.dtype, device=dev)
-        elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
+            out = q.new_empty(q.shape)
+        elif out.shape != q.shape or out.dtype != q.dtype or out.get_device() != dev or not out.is_contiguous():
             raise ValueError("out must be contiguous and match q in shape, type and device")
         if lens.dim() != 1 or table.dim() != 2:
             raise ValueError("lens must be 1-d, table 2-d")
         batch, width = lens.shape[0], table.shape[1]
         if slopes is not None and (slopes.dtype != torch.float32 or tuple(slopes.shape) != (heads,)
-                                   or slopes.device != dev or not slopes.is_contiguous()):
+                                   or slopes.get_device() != dev or not slopes.is_contiguous()):
             raise ValueError("slopes must be a contiguous fp32 tensor [q_heads] on the pages' device")
-        need = LIB.iskv_q8_workspace(heads, self.kv_heads, n, max_new, dt)
-        ws = torch.empty(max(need, 0), dtype=torch.uint8, device=dev)
+        need = self._need.get((heads, max_new, dt))
+        if need is None:
+            with torch.cuda.device(dev):
+                need = LIB.iskv_q8_workspace(heads, self.kv_heads, n, max_new, dt)
+            if len(self._need) < 64:
+                self._need[(heads, max_new, dt)] = need
+        ws = q.new_empty(max(need, 0), dtype=torch.uint8)
         args = _Q8Attention(batch, width, heads, dt, max_new, window, scale, cap, n, q.stride(0), q.data_ptr(),
                             out.data_ptr(), _int32(dev, (batch, width), table, "table"),
                             _int32(dev, (batch,), lens, "lens"), _int32(dev, (batch + 1,), cu, "cu"),
                             None if prefix is None else _int32(dev, (batch,), prefix, "prefix"),
-                            None if slopes is None else slopes.data_ptr(), ws.data_ptr(), need, self._status.data_ptr())
+                            None if slopes is None else slopes.data_ptr(), ws.data_ptr(), need, self._status_at)
         if stream is not None:   # the workspace comes from the current stream's pool
             ws.record_stream(stream)
-        _launch(dev, LIB.iskv_q8_attention, "iskv_q8_attention", ctypes.byref(self._c), ctypes.byref(args),
-                stream=stream)
+        _launch(dev, LIB.iskv_q8_attention, "iskv_q8_attention", self._ref, ctypes.byref(args), stream=stream)
         return out
 
     def status(self) -> int:

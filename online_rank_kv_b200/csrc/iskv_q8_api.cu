@@ -35,7 +35,9 @@ bool all_on_device(const void* const* ptrs, int n) {
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 int check_store(const iskv_q8_pages* s) {
-    if (!s || s->pages < 1 || s->kv_heads < 1 || (int64_t)s->pages * ISKV_PAGE > INT32_MAX) return ISKV_ERR_INVALID_ARG;
+    if (!s || s->pages < 1 || s->kv_heads < 1 || (int64_t)s->pages * ISKV_PAGE > INT32_MAX ||
+        (int64_t)s->pages * s->kv_heads > INT32_MAX)
+        return ISKV_ERR_INVALID_ARG;
     if (s->code != ISKV_CODE_INT8 && s->code != ISKV_CODE_E4M3) return ISKV_ERR_INVALID_ARG;
     if (s->head_dim != kHeadDim || s->page != ISKV_PAGE || s->kv_heads > 65535) return ISKV_ERR_UNSUPPORTED;
     if (!s->k || !s->v || !s->k_scale || !s->v_scale) return ISKV_ERR_INVALID_ARG;

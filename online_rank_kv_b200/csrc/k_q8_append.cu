@@ -1,13 +1,19 @@
 // iskv_q8_append: new K and V rows as 8-bit codes with one scale per page and
 // KV head.
 //
-// A run is the rows of one call that land in one page; the thread that sees a
-// slot which does not follow on from the one before it has found a run's
-// start.  One CTA takes one run of one head, of K or of V: the rows (at most
-// 64 x 128) are held in registers between the pass that finds the largest
-// value and the pass that codes them, so each element is read once and its
-// code written once.  Only where a run continues a page and needs a larger
-// scale are the page's earlier codes read and coded again.
+// A run is the rows of one call that land in one page.  A CTA looks after a
+// window of tokens for one head, of K or of V: its threads compare each slot
+// with the one before, which finds all runs that start in the window and their
+// lengths at once, and then takes them one by one.  The rows of a run (at most
+// 64 x 128) stay in registers, in their own type, between the pass that finds
+// the largest value and the pass that codes them, so each element is read once
+// and its code written once.  Only where a run continues a page and needs a
+// larger scale are the page's earlier codes read and coded again.
+//
+// int8 codes are rint(x / s).  The quotient is taken as a product with 1 / s,
+// which is off by less than 2^-15 for |x / s| <= 127: only where that could
+// move it across a half is the division done.  e4m3 scales are powers of two,
+// and the product is the quotient.
 //
 // Bound by DRAM for prompts (3 bytes per bf16 element) and by launch and load
 // latency for single tokens.
@@ -21,24 +27,35 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kPasses = kPage * kHeadDim / (kThreads * 8);   // 8: 8 elements per thread and pass
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]);
+// 8 elements as they are stored.
+template <typename T> struct Raw;
 template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+struct Raw<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldg(reinterpret_cast<const float4*>(p));
+        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
     }
-}
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+};
+template <>
+struct Raw<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
 
 // The scale that covers values up to `top`.
 template <int CODE>
@@ -52,18 +69,60 @@ __device__ __forceinline__ float scale_of(float top) {
     return __uint_as_float((uint32_t)e << 23);
 }
 
-// x / s as a code; s > 0.  For e4m3 s is a power of two and the quotient exact.
+// Codes of 8 quotients x / s, s > 0, with inv = 1 / s; not finite ones are zeros.
+constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: adding it rounds to a whole number, half to even
 template <int CODE>
-__device__ __forceinline__ uint32_t code4(float a, float b, float c, float d) {
+__device__ __forceinline__ uint2 code8(float (&v)[8], float s, float inv) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = fabsf(v[e]) < INFINITY ? v[e] : 0.f;
+    if constexpr (CODE == ISKV_CODE_INT8) {
+        float y[8], near = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float x = __fmul_rn(v[e], inv);
+            y[e] = __fadd_rn(x, kMagic);
+            near = fmaxf(near, fabsf(__fsub_rn(x, __fsub_rn(y[e], kMagic))));
+        }
+        if (near > 0.4999f) {   // some product may be on the wrong side of a half
+#pragma unroll 1
+            for (int e = 0; e < 8; ++e) {
+                const float x = __fdiv_rn(v[0], s);
+                const float z = __fadd_rn(fminf(fmaxf(x, -127.f), 127.f), kMagic);
+#pragma unroll
+                for (int k = 0; k < 7; ++k) { v[k] = v[k + 1]; y[k] = y[k + 1]; }
+                y[7] = z;
+            }
+        }
+        uint32_t b[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) b[e] = __float_as_uint(y[e]);
+        return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
+                          __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
+    }
+    else {
+        uint16_t c[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c[e]) : "f"(__fmul_rn(v[2 * e + 1], inv)), "f"(__fmul_rn(v[2 * e], inv)));
+        return make_uint2(c[0] | ((uint32_t)c[1] << 16), c[2] | ((uint32_t)c[3] << 16));
+    }
+}
+
+// Values f c of 4 codes as codes again (0 <= f <= 1).
+template <int CODE>
+__device__ __forceinline__ uint32_t recode4(const float (&u)[4], float f) {
+    float x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = __fmul_rn(u[e], f);
     if (CODE == ISKV_CODE_INT8) {
-        // rounded half to even; |x| / s <= 127 up to the rounding of s
-        const int ia = __float2int_rn(fminf(fmaxf(a, -127.f), 127.f)), ib = __float2int_rn(fminf(fmaxf(b, -127.f), 127.f));
-        const int ic = __float2int_rn(fminf(fmaxf(c, -127.f), 127.f)), id = __float2int_rn(fminf(fmaxf(d, -127.f), 127.f));
-        return (ia & 255) | ((ib & 255) << 8) | ((ic & 255) << 16) | ((uint32_t)id << 24);
+        uint32_t b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[e] = __float_as_uint(__fadd_rn(x[e], kMagic));
+        return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
     }
     uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1]), "f"(x[0]));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3]), "f"(x[2]));
     return lo | ((uint32_t)hi << 16);
 }
 
@@ -77,7 +136,7 @@ __device__ __forceinline__ void decode4(uint32_t x, float (&v)[4]) {
 }
 
 template <int CODE, typename T>
-__global__ void __launch_bounds__(kThreads) q8_append_kernel(const AppendArgs p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 5) q8_append_kernel(const AppendArgs p) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int head = blockIdx.y, which = blockIdx.z;
     const T* x = static_cast<const T*>(which ? p.x[1] : p.x[0]);
@@ -85,55 +144,71 @@ __global__ void __launch_bounds__(kThreads) q8_append_kernel(const AppendArgs p)
     uint8_t* store = static_cast<uint8_t*>(which ? p.store[1] : p.store[0]);
     float* scale = which ? p.scale[1] : p.scale[0];
     const int64_t t0 = (int64_t)blockIdx.x * p.window;
-    const int64_t t1 = t0 + p.window < p.n ? t0 + p.window : p.n;
     const int64_t n_slots = (int64_t)p.pages * kPage;
     __shared__ float s_top[kThreads / 32];
-    __shared__ int s_run[2];
+    __shared__ uint32_t s_break[kThreads / 32];   // tokens t0 + 0 .. 127: it does not go on where the one before ended
+    __shared__ uint32_t s_start[2];               // tokens of the window where a run starts
+    __shared__ int s_slot[kPage];
 
-    for (int64_t i = t0; i < t1; ++i) {   // uniform over the CTA
-        const int64_t slot = p.slots[i];
-        if (slot < 0 || slot >= n_slots) {
-            if (slot != -1 && t == 0 && p.status) atomicMin(p.status, ISKV_ERR_INVALID_ARG);
-            continue;
+    {
+        const int64_t i = t0 + t;
+        const bool in = i < p.n;
+        const int64_t slot = in ? p.slots[i] : -1;
+        const int64_t before = in && i > 0 ? p.slots[i - 1] : -1;
+        const bool good = slot >= 0 && slot < n_slots;
+        if (in && t < p.window && !good && slot != -1 && p.status) atomicMin(p.status, ISKV_ERR_INVALID_ARG);
+        const uint32_t m = __ballot_sync(0xffffffffu, !good || slot % kPage == 0 || before != slot - 1);
+        const uint32_t g = __ballot_sync(0xffffffffu, good && t < p.window);
+        if (lane == 0) {
+            s_break[warp] = m;
+            if (warp < 2) s_start[warp] = m & g;
         }
+        if (t < kPage) s_slot[t] = (int)slot;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (uint64_t todo = s_start[0] | (uint64_t)s_start[1] << 32; todo != 0; todo &= todo - 1) {   // uniform over the CTA
+        const int j = __ffsll((long long)todo) - 1;
+        const int64_t i = t0 + j, slot = s_slot[j];
         const int row0 = (int)(slot % kPage);
-        if (i > 0 && row0 != 0 && p.slots[i - 1] == slot - 1) continue;   // inside a run
-        // rows of the run: how far the slots go on one by one inside the page
-        if (warp < 2) {
-            const bool on = t < kPage - row0 && i + t < p.n && p.slots[i + t] == slot + t;
-            const uint32_t m = __ballot_sync(0xffffffffu, on);
-            if (lane == 0) s_run[warp] = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
+        // rows of the run: up to the next break (within 64 tokens, as the page ends)
+        int n;
+        {
+            const int a = j + 1;
+            uint32_t m = a < 128 ? s_break[a >> 5] >> (a & 31) : 1u;
+            n = a;
+            if (m == 0u) {
+                int w = (a >> 5) + 1;
+                while (w < kThreads / 32 && s_break[w] == 0u) ++w;
+                n = w < kThreads / 32 ? 32 * w + __ffs(s_break[w]) - 1 : 128;
+            } else {
+                n = a + __ffs(m) - 1;
+            }
+            n = min(n - j, kPage - row0);
         }
-        __syncthreads();
-        const int n = s_run[0] < 32 ? s_run[0] : 32 + s_run[1];
 
         // 16 threads per row, 8 rows per pass
         const int col = (t & 15) * 8;
-        float v[kPasses][8];
+        Raw<T> v[kPasses];
         float top = 0.f;
         bool bad = false;
 #pragma unroll
         for (int s = 0; s < kPasses; ++s) {
             const int r = s * (kThreads / 16) + (t >> 4);
-            if (r < n) {
-                load8<T>(x + (i + r) * stride + head * kHeadDim + col, v[s]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[s][e] = 0.f;
-            }
+            if (r < n) v[s].load(x + (i + r) * stride + head * kHeadDim + col);
+            else v[s].zero();
         }
 #pragma unroll
-        for (int s = 0; s < kPasses; ++s)
+        for (int s = 0; s < kPasses; ++s) {
+            float u[8];
+            v[s].get(u);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float m = fabsf(v[s][e]);
-                if (!(m < INFINITY)) {   // infinities and NaN are stored as zeros
-                    bad = true;
-                    v[s][e] = 0.f;
-                } else {
-                    top = fmaxf(top, m);
-                }
+                const float m = fabsf(u[e]);
+                bad = bad || !(m < INFINITY);   // infinities and NaN are stored as zeros
+                top = fmaxf(top, m < INFINITY ? m : 0.f);
             }
+        }
         if (bad && p.status) atomicMin(p.status, ISKV_ERR_RANGE);
         top = warp_max(top);
         if (lane == 0) s_top[warp] = top;
@@ -154,12 +229,13 @@ __global__ void __launch_bounds__(kThreads) q8_append_kernel(const AppendArgs p)
                 uint2 c = *at;
                 float u[4];
                 decode4<CODE>(c.x, u);
-                c.x = code4<CODE>(__fmul_rn(u[0], f), __fmul_rn(u[1], f), __fmul_rn(u[2], f), __fmul_rn(u[3], f));
+                c.x = recode4<CODE>(u, f);
                 decode4<CODE>(c.y, u);
-                c.y = code4<CODE>(__fmul_rn(u[0], f), __fmul_rn(u[1], f), __fmul_rn(u[2], f), __fmul_rn(u[3], f));
+                c.y = recode4<CODE>(u, f);
                 *at = c;
             }
         }
+        const float inv = now > 0.f ? __fdiv_rn(1.f, now) : 0.f;
 #pragma unroll
         for (int s = 0; s < kPasses; ++s) {
             const int r = s * (kThreads / 16) + (t >> 4);
@@ -167,14 +243,12 @@ __global__ void __launch_bounds__(kThreads) q8_append_kernel(const AppendArgs p)
             uint2 c = make_uint2(0u, 0u);
             if (now > 0.f) {
                 float u[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] = __fdiv_rn(v[s][e], now);
-                c.x = code4<CODE>(u[0], u[1], u[2], u[3]);
-                c.y = code4<CODE>(u[4], u[5], u[6], u[7]);
+                v[s].get(u);
+                c = code8<CODE>(u, now, inv);
             }
             *reinterpret_cast<uint2*>(base + (row0 + r) * kHeadDim + col) = c;
         }
-        __syncthreads();   // s_run and s_top are free again
+        __syncthreads();   // s_top is free again
     }
 }
 

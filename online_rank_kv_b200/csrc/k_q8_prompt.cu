@@ -776,6 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int cta = blockIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;");   // the join may come up; it waits for this grid's end
 
     // ---- this CTA's range -------------------------------------------------
     // pairs of query tiles up to each request, then cost up to each pair

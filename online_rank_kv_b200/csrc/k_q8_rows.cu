@@ -27,12 +27,16 @@
 // Work.  Requests, heads, row tiles and 32-token steps are numbered through;
 // every CTA finds its equal share of the steps from the lengths itself (one
 // pass over the requests, no plan on the host) and every warp its share of
-// that, so lengths may differ freely.  A warp runs its own three-stage
-// cp.async pipeline (4 KB of K and 4 KB of V per stage) and never waits for
-// another warp until its share is done.  What one warp finishes alone is
+// that, so lengths may differ freely.  A warp runs its own pipeline of tensor
+// copies (a stage is 4 KB of K and 4 KB of V, swizzled as the fragment loads
+// want them; one lane issues both) and never waits for another warp until its
+// share is done.  What one warp finishes alone is
 // written at once; what several warps share is joined in the CTA, what several
 // CTAs share by a second small kernel.
+#include <cuda.h>
+
 #include "q8_common.cuh"
+#include "tc_util.cuh"
 
 namespace iskv {
 namespace q8 {
@@ -41,8 +45,8 @@ namespace {
 
 // Warps and pipeline stages per warp.  The loop is bound by the latency of its
 // own instructions, so the light variant takes 12 warps of 168 registers with
-// two stages each (measured against 8 warps with three: 8 x 32K tokens 117 ->
-// __ us); two row tiles or fp32 parts need more registers and take 8.
+// two stages each (measured against 8 warps with three: 96 ragged requests of up
+// to 16K tokens 353 -> 317 us, 8 x 32K tokens 117 -> 116 us); two row tiles or fp32 parts need more registers and take 8.
 template <int NT, bool F32>
 struct Shape {
     static constexpr int kWarps = rows_warps(NT, F32);
@@ -56,12 +60,13 @@ using Req = Seen<kStepTokens>;
 
 __device__ __forceinline__ int tiles_of(const AttnArgs& p, int n) { return (n + p.tq - 1) / p.tq; }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// A box of the tensor map: 32 rows of 128 codes from row `row` of (page, head) `block` on.
+__device__ __forceinline__ void copy_step(uint32_t dst, const CUtensorMap* map, int row, int block, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(0), "r"(row), "r"(block), "r"(tc::smem_u32(bar))
+        : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -142,45 +147,59 @@ __device__ __forceinline__ void store_out(const AttnArgs& p, int64_t at, const f
     }
 }
 
-// Joins `n` partials of R rows, read through `at(i)` (the i-th partial's
-// index), into one: either the final rows of `item` or partial `to`.
-template <int R, bool F32, typename At>
-__device__ __forceinline__ void join(const AttnArgs& p, int n, At at, int to, int b, int item) {
-    const Req r = seen_of<kStepTokens>(p, b);
-    const int tiles = tiles_of(p, r.n), h = item / tiles, tile = item % tiles;
+// One row's sum over partials i = first, first + step, ... < n (at(i): the i-th
+// partial's row in the workspace), relative to the largest of their maxima: the
+// lane's four columns in o, the denominator in l.
+template <typename At>
+__device__ __forceinline__ void sum_parts(const AttnArgs& p, int first, int step, int n, At at, int lane, float& M, float& l, float (&o)[4]) {
+    M = -INFINITY;
+    l = 0.f;
+    o[0] = o[1] = o[2] = o[3] = 0.f;
 #pragma unroll 1
-    for (int e = threadIdx.x; e < R * 32; e += blockDim.x) {
-        const int row = e >> 5, d = (e & 31) * 4, k = row / p.g;
-        const int token = tile * p.tq + k, head = h * p.g + row - k * p.g;
-        if (k >= p.tq || token >= r.n) continue;
-        float M = -INFINITY;
+    for (int i0 = first; i0 < n; i0 += 32 * step) {   // 32 partials at a time, their maxima in the lanes
+        const int i = i0 + lane * step;
+        const float2 ml = i < n ? *reinterpret_cast<const float2*>(p.ml + at(i) * 2) : make_float2(-INFINITY, 0.f);
+        const float now = fmaxf(M, warp_max(ml.x));
+        const float base = now == -INFINITY ? 0.f : now;
+        const float f = ex2(ml.x - base), g = ex2(M - base);
+        l = l * g + warp_sum(f * ml.y);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] *= g;
+        M = now;
+        const int m = min(32, (n - i0 + step - 1) / step);
 #pragma unroll 4
-        for (int i = 0; i < n; ++i) M = fmaxf(M, p.ml[((int64_t)at(i) * R + row) * 2]);
-        const float base = M == -INFINITY ? 0.f : M;
-        float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const int64_t k = (int64_t)at(i) * R + row;
-            const float2 ml = *reinterpret_cast<const float2*>(p.ml + k * 2);
-            const float4 v = *reinterpret_cast<const float4*>(p.part + k * kHeadDim + d);
-            const float w = ex2(ml.x - base);
-            l += w * ml.y;
+        for (int k = 0; k < m; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(p.part + at(i0 + k * step) * kHeadDim + 4 * lane);
+            const float w = __shfl_sync(0xffffffffu, f, k);
             o[0] += w * v.x;
             o[1] += w * v.y;
             o[2] += w * v.z;
             o[3] += w * v.w;
         }
-        if (to < 0) {
-            const float inv = l > 0.f ? __fdividef(1.f, l) : (l == 0.f ? 0.f : l);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] *= inv;
-            store_out<F32, 4>(p, ((int64_t)(r.first + token) * p.kv_heads * p.g + head) * kHeadDim + d, o);
-        } else {
-            const int64_t k = (int64_t)to * R + row;
-            *reinterpret_cast<float4*>(p.part + k * kHeadDim + d) = make_float4(o[0], o[1], o[2], o[3]);
-            if (d == 0) *reinterpret_cast<float2*>(p.ml + k * 2) = make_float2(M, l);
-        }
     }
+}
+
+// The joined row: to its place in out, or to partial row `to` (>= 0).
+template <bool F32>
+__device__ __forceinline__ void put_row(const AttnArgs& p, int64_t out_at, int64_t to, float M, float l, float (&o)[4], int lane) {
+    if (to < 0) {
+        const float inv = l > 0.f ? __fdividef(1.f, l) : (l == 0.f ? 0.f : l);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] *= inv;
+        store_out<F32, 4>(p, out_at + 4 * lane, o);
+    } else {
+        *reinterpret_cast<float4*>(p.part + to * kHeadDim + 4 * lane) = make_float4(o[0], o[1], o[2], o[3]);
+        if (lane == 0) *reinterpret_cast<float2*>(p.ml + to * 2) = make_float2(M, l);
+    }
+}
+
+// Row `row` of (request, item): its place in out; false where it has none.
+__device__ __forceinline__ bool place_of(const AttnArgs& p, int b, int item, int row, int64_t* at) {
+    const Req r = seen_of<kStepTokens>(p, b);
+    const int tiles = tiles_of(p, r.n), h = item / tiles, tile = item - h * tiles;
+    const int k = row / p.g, token = tile * p.tq + k, head = h * p.g + row - k * p.g;
+    *at = ((int64_t)(r.first + token) * p.kv_heads * p.g + head) * kHeadDim;
+    return k < p.tq && token < r.n;
 }
 
 // Meta words per CTA: [0] whether its partial 0 ends an item; [1] CTAs that
@@ -189,18 +208,27 @@ __device__ __forceinline__ void join(const AttnArgs& p, int n, At at, int to, in
 constexpr int kMeta = 4;
 
 template <int CODE, int NT, bool F32, bool MOD>
-__global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(const AttnArgs p) {
+__global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(const AttnArgs p, const __grid_constant__ CUtensorMap map_k,
+                                                                               const __grid_constant__ CUtensorMap map_v) {
     constexpr int kWarps = Shape<NT, F32>::kWarps, kThreads = Shape<NT, F32>::kThreads, kStages = Shape<NT, F32>::kStages;
     constexpr int kPartsPerCta = 2 * kWarps + 2;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t dyn[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
     __shared__ int64_t s_scan[kWarps], s_off[kWarps];
     __shared__ int s_b[kWarps];
     __shared__ Part s_part[kWarps][2];
     __shared__ int s_page[kWarps][kStages];
+    __shared__ uint64_t s_full[kWarps][kStages];
     constexpr int R = 8 * NT, PARTS = F32 ? 2 : 1;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int r = lane >> 2, q = lane & 3;
     const int cta = blockIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;");   // the join may come up; it waits for this grid's end
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) tc::mbar_init(&s_full[warp][i], 1);
+        tc::fence_mbar_init();
+    }
 
     // ---- this CTA's and this warp's share of the steps --------------------
     const int chunk = (p.batch + kThreads - 1) / kThreads;
@@ -270,6 +298,7 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
         }
     }
 
+    int gave_up = 0;
     if (n_steps > 0) {
         Cursor in, at;
         at.b = s_b[warp];
@@ -298,35 +327,31 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
             return tok < c.r.len ? p.table[(int64_t)c.b * p.width + tok / kPage] : -1;
         };
         int page = page_of(in), fill = 0, stage = 0;
+        uint32_t phase = 0;   // a bit per stage
+        bool failed = false;
         // kStages - 1 steps are on their way before the first is used
 #pragma unroll 1
         for (int ahead = 1 - kStages; left > 0; ++ahead) {
             if (to_issue > 0) {
                 const int tok = in.r.step_of(in.step) * kStepTokens;
                 const bool ok = page >= 0 && page < p.pages;
-                const int rows = ok ? in.r.len - tok : 0;   // rows of the step that are stored
-                const int ch = lane & 7, row = lane >> 3;
-                const int64_t src = ((int64_t)(ok ? page : 0) * p.kv_heads + in.h) * (kPage * kHeadDim) +
-                                    ((tok % kPage) + row) * kHeadDim + ch * 16;
-                const uint8_t* sk8 = p.k + src;
-                const uint8_t* sv8 = p.v + src;
-                const uint32_t dst = ring_at + fill * kStageBytes + row * kHeadDim;
-                const uint32_t d0 = dst + ((ch ^ row) << 4), d1 = dst + ((ch ^ (row + 4)) << 4);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t d = ((i & 1) ? d1 : d0) + i * 4 * kHeadDim;
-                    const uint32_t bytes = row + 4 * i < rows ? 16u : 0u;   // rows behind the end read as zeros
-                    cp16(d, sk8 + i * 4 * kHeadDim, bytes);
-                    cp16(d + kStoreBytes, sv8 + i * 4 * kHeadDim, bytes);
+                if (lane == 0) {
+                    s_page[warp][fill] = ok ? page : -1;
+                    uint64_t* bar = &s_full[warp][fill];
+                    const uint32_t dst = ring_at + fill * kStageBytes;
+                    tc::mbar_arrive_expect_tx(bar, ok ? kStageBytes : 0);
+                    if (ok) {
+                        const int block = page * p.kv_heads + in.h;
+                        copy_step(dst, &map_k, tok % kPage, block, bar);
+                        copy_step(dst + kStoreBytes, &map_v, tok % kPage, block, bar);
+                    }
                 }
-                if (lane == 0) s_page[warp][fill] = ok ? page : -1;
                 fill = fill + 1 == kStages ? 0 : fill + 1;
                 if (--to_issue > 0) {
                     in.next(p);
                     page = page_of(in);
                 }
             }
-            cp_commit();
             if (ahead < 0) continue;
 
             if (fresh) {   // an item begins: its queries
@@ -399,11 +424,30 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
                 }
             }
 
-            cp_wait<kStages - 1>();
             __syncwarp();
+            if (!tc::mbar_try_wait(&s_full[warp][stage], (phase >> stage) & 1) &&
+                !tc::mbar_wait(&s_full[warp][stage], (phase >> stage) & 1, clock64() + tc::kWaitCycles))
+                failed = true;
+            if (__any_sync(0xffffffffu, failed)) {   // out is left incomplete
+                failed = true;
+                gave_up = 1;
+                if (lane == 0 && p.status) atomicMin(p.status, ISKV_ERR_DEVICE_TIMEOUT);
+                break;
+            }
+            phase ^= 1u << stage;
             const int this_page = s_page[warp][stage];
             const int tok = at.r.step_of(at.step) * kStepTokens;
             const int stop = this_page < 0 ? 0 : at.r.len;      // stored tokens end here
+            if (tok + kStepTokens > stop) {
+                // what stands behind the last token (codes of an earlier owner, which
+                // may be NaN) becomes zeros; hidden keys need no such care
+#pragma unroll 1
+                for (int e = lane; e < kStoreBytes / 16; e += 32)
+                    if (tok + (e >> 3) >= stop)
+                        *reinterpret_cast<uint4*>(ring + stage * kStageBytes + kStoreBytes + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+                tc::fence_async_smem();   // before the next copy into this stage
+                __syncwarp();
+            }
             const int64_t block = (int64_t)max(this_page, 0) * p.kv_heads + at.h;
             const float sk = __ldg(p.k_scale + block);
             float sv = __ldg(p.v_scale + block);
@@ -589,36 +633,38 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
             }
             if (left > 0) at.next(p);
         }
-        cp_wait<0>();
+    }
+
+    if (__syncthreads_or(gave_up)) {
+        // copies may be on their way to warps that have given up: they land within
+        // microseconds; the CTA ends long after
+        const long long until = clock64() + 20000000;
+        while (clock64() < until) __nanosleep(1000);
     }
 
     // ---- items that several warps of this CTA share ------------------------
-    __syncthreads();
+    // A group is the parts of one item, which follow each other; (group, row)
+    // pairs are dealt to the warps.
     if (t < kMeta) p.meta[cta * kMeta + t] = 0;
+    const int64_t id = lane < 2 * kWarps ? s_part[lane >> 1][lane & 1].id : -1;
+    const uint32_t there = __ballot_sync(0xffffffffu, id >= 0);
+    const uint32_t below = there & ((1u << lane) - 1u);
+    const int64_t id_before = __shfl_sync(0xffffffffu, id, below ? 31 - __clz(below) : 0);
+    const uint32_t heads = __ballot_sync(0xffffffffu, id >= 0 && (below == 0 || id_before != id));
     __syncthreads();
-    int i = 0;
+    const int groups = __popc(heads);
 #pragma unroll 1
-    while (i < 2 * kWarps) {
-        const Part a = s_part[i >> 1][i & 1];
-        if (a.id < 0) {
-            ++i;
-            continue;
-        }
-        int list[2 * kWarps], n = 0, end = i, ends = 0;
-#pragma unroll 1
-        while (end < 2 * kWarps) {
-            const Part z = s_part[end >> 1][end & 1];
-            if (z.id >= 0) {
-                if (z.id != a.id) break;
-                list[n++] = end;
-                ends = z.ends;
-            }
-            ++end;
-        }
+    for (int e = warp; e < groups * R; e += kWarps) {
+        const int grp = e / R, row = e % R;
+        const int first = __fns(heads, 0, grp + 1);
+        const int next = grp + 1 < groups ? (int)__fns(heads, 0, grp + 2) : 32;
+        const uint32_t mine_m = there & (next < 32 ? (1u << next) - 1u : 0xffffffffu) & ~((1u << first) - 1u);
+        const int last_e = 31 - __clz(mine_m);
+        const Part a = s_part[first >> 1][first & 1];
+        const int ends = s_part[last_e >> 1][last_e & 1].ends;
         const int b = (int)(a.id >> 32), item = (int)(uint32_t)a.id;
-        const int to = a.begins && ends ? -1 : cta * kPartsPerCta + 2 * kWarps + (a.begins ? 1 : 0);
-        join<R, F32>(p, n, [&](int k) { return cta * kPartsPerCta + list[k]; }, to, b, item);
-        if (t == 0 && to >= 0) {
+        const bool final = a.begins && ends;
+        if (row == 0 && lane == 0 && !final) {
             int* m = p.meta + cta * kMeta;
             if (!a.begins) {
                 m[0] = ends;
@@ -628,51 +674,102 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
                 m[3] = item;
             }
         }
-        i = end;
+        int64_t out_at;
+        if (!place_of(p, b, item, row, &out_at)) continue;
+        float M, l, o[4];
+        sum_parts(p, 0, 1, __popc(mine_m),
+                  [&](int k) { return (int64_t)(cta * kPartsPerCta + (int)__fns(mine_m, 0, k + 1)) * R + row; }, lane, M, l, o);
+        put_row<F32>(p, out_at, final ? -1 : (int64_t)(cta * kPartsPerCta + 2 * kWarps + (a.begins ? 1 : 0)) * R + row, M, l, o, lane);
     }
 }
 
-// Items that several CTAs share: CTA c joins the one that its partial 1 begins
-// with the partials 0 of the CTAs after it, up to the one that ends it.
+// Items that several CTAs share: CTA c joins a row of the one that its partial
+// 1 begins with the partials 0 of the CTAs after it, up to the one that ends it.
+// Each warp sums some of the partials.
 template <int NT, bool F32>
 __global__ void __launch_bounds__(256) q8_join_kernel(const AttnArgs p) {
     constexpr int R = 8 * NT, kWarps = Shape<NT, F32>::kWarps, kPartsPerCta = 2 * kWarps + 2;
-    const int cta = blockIdx.x;
+    const int cta = blockIdx.x, row = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ float s_ml[8][2], s_o[8][kHeadDim];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int* m = p.meta + cta * kMeta;
-    if (m[1] == 0) return;
-    __shared__ int s_n;
-    if (threadIdx.x < 32) {   // how many CTAs follow
-        int n = 0;
-        for (int c0 = cta + 1; c0 < p.ctas; c0 += 32) {
-            const int c = c0 + (int)threadIdx.x;
-            const bool e = c < p.ctas && p.meta[c * kMeta] != 0;
-            const uint32_t hit = __ballot_sync(0xffffffffu, e);
-            if (hit) {
-                n += __ffs(hit);
-                break;
-            }
-            n += 32;
-        }
-        if (threadIdx.x == 0) s_n = min(n, p.ctas - 1 - cta);
+    const int4 m = *reinterpret_cast<const int4*>(p.meta + cta * kMeta);
+    if (m.y == 0) return;
+    int64_t out_at;
+    if (!place_of(p, m.z, m.w, row, &out_at)) return;
+    int n = 1;   // partials: how many CTAs follow
+#pragma unroll 1
+    for (int c0 = cta + 1; c0 < p.ctas; c0 += 32) {
+        const uint32_t hit = __ballot_sync(0xffffffffu, c0 + lane < p.ctas && p.meta[(c0 + lane) * kMeta] != 0);
+        n += hit ? __ffs(hit) : 32;
+        if (hit) break;
     }
+    n = min(n, p.ctas - cta);
+    float M, l, o[4];
+    sum_parts(p, warp, 8, n,
+              [&](int k) { return (int64_t)((cta + k) * kPartsPerCta + 2 * kWarps + (k == 0 ? 1 : 0)) * R + row; }, lane, M, l, o);
+    if (lane == 0) {
+        s_ml[warp][0] = M;
+        s_ml[warp][1] = l;
+    }
+    *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = make_float4(o[0], o[1], o[2], o[3]);
     __syncthreads();
-    join<R, F32>(p, 1 + s_n,
-                 [&](int k) { return (cta + k) * kPartsPerCta + 2 * kWarps + (k == 0 ? 1 : 0); }, -1, m[2], m[3]);
+    if (warp > 0) return;
+    float top = M;
+#pragma unroll
+    for (int w = 1; w < 8; ++w) top = fmaxf(top, s_ml[w][0]);
+    const float base = top == -INFINITY ? 0.f : top;
+    l = 0.f;
+    o[0] = o[1] = o[2] = o[3] = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        const float f = ex2(s_ml[w][0] - base);
+        const float4 v = *reinterpret_cast<const float4*>(&s_o[w][4 * lane]);
+        l += f * s_ml[w][1];
+        o[0] += f * v.x;
+        o[1] += f * v.y;
+        o[2] += f * v.z;
+        o[3] += f * v.w;
+    }
+    put_row<F32>(p, out_at, -1, top, l, o, lane);
+}
+
+// The codes of one store as [pages * kv_heads][64][128] bytes, copied 32 rows at
+// a time with the 128-byte swizzle (chunk c of row t stands at c ^ (t & 7)).
+bool tensor_map(const AttnArgs& a, const uint8_t* codes, CUtensorMap* map) {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<Encode>(f);
+    }();
+    if (!encode) return false;
+    const cuuint64_t dims[3] = {kHeadDim, kPage, (cuuint64_t)a.pages * a.kv_heads};
+    const cuuint64_t strides[2] = {kHeadDim, kPage * kHeadDim};
+    const cuuint32_t box[3] = {kHeadDim, kStepTokens, 1}, step[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(codes), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int CODE, int NT, bool F32, bool MOD>
 cudaError_t run(const AttnArgs& a, cudaStream_t s) {
     using S = Shape<NT, F32>;
-    constexpr int kSmemBytes = S::kWarps * S::kStages * kStageBytes;
+    constexpr int kSmemBytes = S::kWarps * S::kStages * kStageBytes + 1024;
     static SmemOnce once;
     cudaError_t e = once.set(q8_rows_kernel<CODE, NT, F32, MOD>, kSmemBytes);
     if (e != cudaSuccess) return e;
-    q8_rows_kernel<CODE, NT, F32, MOD><<<a.ctas, S::kThreads, kSmemBytes, s>>>(a);
+    CUtensorMap map_k, map_v;
+    if (!tensor_map(a, a.k, &map_k) || !tensor_map(a, a.v, &map_v)) return cudaErrorInvalidValue;
+    q8_rows_kernel<CODE, NT, F32, MOD><<<a.ctas, S::kThreads, kSmemBytes, s>>>(a, map_k, map_v);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.ctas);
+    cfg.gridDim = dim3(a.ctas, 8 * NT);
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
