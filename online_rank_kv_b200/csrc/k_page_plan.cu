@@ -160,17 +160,31 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const iskv_page_pla
         a.lens_out[b] = ended ? 0 : s_len[b] + (s_cu[b + 1] - s_cu[b]);
     }
     for (int b = gt; b <= B; b += step) a.cu[b] = s_cu[b];
-    for (int i = gt; i < a.tokens; i += step) {
-        int slot = -1;
-        if (i < added) {
-            const int b = last_at_most(s_cu, B, i);
-            const int pos = s_len[b] + (i - s_cu[b]);
-            const int block = pos / kPage, had = (s_len[b] + kPage - 1) / kPage;
-            const int page = block < had ? a.table[(int64_t)b * a.width + block]
-                                         : page_new(s_need[b] + block - had);
-            if (page >= 0 && page < a.pages) slot = page * kPage + pos % kPage;
+    // where there are many slots, a thread's four follow each other: one search,
+    // and mostly one page
+    const int per = a.tokens <= step ? 1 : 4;
+    for (int i0 = per * gt; i0 < a.tokens; i0 += per * step) {
+        int b = i0 < added ? last_at_most(s_cu, B, i0) : B, of = -1, base = -1;
+#pragma unroll 1
+        for (int e = 0; e < per; ++e) {
+            const int i = i0 + e;
+            int slot = -1;
+            if (i < added) {
+                while (i >= s_cu[b + 1]) {
+                    ++b;
+                    of = -1;
+                }
+                const int pos = s_len[b] + (i - s_cu[b]), block = pos / kPage;
+                if (block != of) {
+                    of = block;
+                    const int had = (s_len[b] + kPage - 1) / kPage;
+                    const int page = block < had ? a.table[(int64_t)b * a.width + block] : page_new(s_need[b] + block - had);
+                    base = page >= 0 && page < a.pages ? page * kPage : -1;
+                }
+                slot = base < 0 ? -1 : base + pos % kPage;
+            }
+            if (i < a.tokens) a.slots[i] = slot;
         }
-        a.slots[i] = slot;
     }
     for (int j = gt; j < fresh; j += step) {
         const int b = last_at_most(s_need, B, j);
@@ -187,9 +201,9 @@ cudaError_t launch_page_plan(const iskv_page_plan_args& a, cudaStream_t s) {
     static SmemOnce once;
     const cudaError_t e = once.set(page_plan_kernel, ((size_t)4 * kMaxBatch + 3) * sizeof(int));
     if (e != cudaSuccess) return e;
-    // one CTA writes about 2048 slots in the time the sums take
+    // four slots per thread, up to what a portable cluster holds
     int ctas = 1;
-    while (ctas < 8 && (int64_t)ctas * 2048 < a.tokens) ctas *= 2;
+    while (ctas < 8 && (int64_t)ctas * 4 * kThreads < a.tokens) ctas *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);

@@ -17,9 +17,10 @@
 //   warps 12, 14    issue the MMAs of tile 0 and of tile 1: S_i = Q_i K^T,
 //                   O_i += P_i V
 //   warp 13         walks the CTA's work, looks up pages and scales 32 steps at
-//                   a time, tells the others about each step through a ring of
-//                   eight descriptions, and copies its codes in (8 KB per
-//                   operand by the bulk copy engine)
+//                   a time and tells the others about each step through a ring
+//                   of eight descriptions
+//   warp 15         copies the steps' codes in (8 KB per operand by the bulk copy
+//                   engine)
 // Each tile has two score buffers of 64 columns: a tile's softmax works on one
 // page's scores while the MMAs of the page before (its values, then the scores
 // of the page after next, into the buffer that it frees) run, so neither waits
@@ -55,7 +56,7 @@ constexpr int kSoftmaxWarps = 8, kCodeWarps = 4;
 // launch has.
 constexpr int kThreads = 32 * (kSoftmaxWarps + kCodeWarps + 4);
 constexpr int kSoftmaxRegs = 176, kCodeRegs = 80, kOtherRegs = 80;
-constexpr int kMmaWarp = kSoftmaxWarps + kCodeWarps, kWalkWarp = kMmaWarp + 1;
+constexpr int kMmaWarp = kSoftmaxWarps + kCodeWarps, kWalkWarp = kMmaWarp + 1, kCopyWarp = kMmaWarp + 3;
 constexpr float kShift = 7.f;
 constexpr float kRaise = 8.f;
 // What the start and the end of a pair cost, in steps, where work is split.
@@ -66,7 +67,7 @@ constexpr int kFirst = 1, kEnd = 2;     // of a piece; of the work
 struct Step {
     int flags, key0;
     int left;               // steps of the piece that follow
-    int there;              // its page exists
+    int page;               // -1: there is none
     float sk, lsv, isv;     // key scale, log2 of the value scale, its inverse
     int len, pre, n, first; // the request: tokens, prefix, queries, first query row
     int token0, h;          // the pair's first query, KV head
@@ -158,6 +159,18 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
+}
+
+// 32 bytes to global memory: one store where the address allows it.
+__device__ __forceinline__ void store32(void* to, const uint32_t (&v)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                     "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(to)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4*>(to)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
 }
 
 // Shared-memory operand with 128-byte rows, 128-byte swizzle (the 16-byte chunk
@@ -305,8 +318,14 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
         load(sh.step[0]);
     }
 
+    // of the piece before: running maximum and sum, its place
+    float M = -INFINITY, l = 0.f;
+    int64_t place = -1;
+    int slot = -1;
+    bool more = true;
+    const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0, wide_part = (reinterpret_cast<uintptr_t>(p.part) & 31) == 0;
     for (int n = 0;;) {   // pieces
-        // ---- queries ----
+        // ---- queries (stored even where there are none any more: nothing reads them) ----
         float rowf = 0.f;
 #pragma unroll
         for (int z = 0; z < 16; ++z) {
@@ -334,16 +353,57 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
             if ((lane >> 1) == z)
                 rowf = __uint_as_float((uint32_t)(127 - mine) << 23) * (p.scale * (MOD ? 1.f : kLog2e));
         }
-        tc::fence_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sh.q_full[i]);
+        if (more) {
+            tc::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sh.q_full[i]);
+        }
+        // ---- results of the piece before, while the next one's scores start ----
+        if (n > 0) {
+            const float inv = l > 0.f ? __fdiv_rn(1.f, l) : (l == 0.f ? 0.f : l);
+            const int64_t at = (int64_t)slot * (2 * kM) + i * kM + row;
+            __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(p.out) + place;
+            float* const part = p.part + at * kHeadDim;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                __syncwarp();
+                tmem_ld32(tO + 32 * c, o);
+                tmem_wait(o);
+                if (place < 0) {
+                } else if (slot < 0) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 16) {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int z = 0; z < 8; ++z) {
+                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * z]) * inv,
+                                                                            __uint_as_float(o[e + 2 * z + 1]) * inv);
+                            v[z] = *reinterpret_cast<const uint32_t*>(&b2);
+                        }
+                        store32(out + 32 * c + e, v, wide);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        const uint32_t v[8] = {o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5], o[e + 6], o[e + 7]};
+                        store32(part + 32 * c + e, v, wide_part);
+                    }
+                }
+            }
+            if (slot >= 0 && place >= 0) *reinterpret_cast<float2*>(p.ml + at * 2) = make_float2(M, l);
+            tc::tc_fence_before();
+            __syncwarp();
+            if (!more) return;
+        }
 
         const int n_q = sh.step[n % kSteps].n, len = sh.step[n % kSteps].len, pre = sh.step[n % kSteps].pre;
         const int pos = len - n_q + min(token, n_q - 1);
         const int see_from = p.window > 0 ? max(-1, pos - p.window) : -1;   // sees (see_from, pos] and the prefix
         const float slope = MOD && p.slopes && on ? p.slopes[head] * kLog2e : 0.f;
         const int wp_min = __reduce_min_sync(0xffffffffu, pos), wp_max = __reduce_max_sync(0xffffffffu, pos);
-        float M = -INFINITY, l = 0.f;
+        M = -INFINITY;
+        l = 0.f;
 
         for (bool first = true;; first = false) {   // steps
             const Step& st = sh.step[n % kSteps];
@@ -357,7 +417,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
             tmem_ld32(tSn, *reinterpret_cast<uint32_t(*)[32]>(s));
             tmem_ld32(tSn + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
             const int key0 = st.key0;
-            const bool there = st.there;
+            const bool there = st.page >= 0;
             const bool clear = there && key0 + kN <= len &&
                                ((key0 + kN - 1 <= wp_min && (p.window == 0 || key0 > wp_max - p.window)) || key0 + kN <= pre);
             // the smallest normal number in place of zero keeps hidden scores at -inf
@@ -464,80 +524,22 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
             ++n;
         }
 
-        // ---- end of the piece; the next one's queries are loaded meanwhile ----
-        const Step& st = sh.step[n % kSteps];
-        const int slot = st.slot;
-        const int64_t own = on ? ((int64_t)(st.first + token) * p.kv_heads * p.g + head) * kHeadDim : -1;
-        const bool own_on = on;
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sh.info_empty[n % kSteps]);
-        const int nx = n + 1;
-        bool ok = __all_sync(0xffffffffu, wait_for(sh, &sh.info_full[nx % kSteps], (nx / kSteps) & 1));
+        // ---- end of the piece: the next one's queries, and the last values ----
+        {
+            const Step& st = sh.step[n % kSteps];
+            slot = st.slot;
+            place = on ? ((int64_t)(st.first + token) * p.kv_heads * p.g + head) * kHeadDim : -1;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sh.info_empty[n % kSteps]);
+        }
+        const int last = n++;
+        bool ok = __all_sync(0xffffffffu, wait_for(sh, &sh.info_full[n % kSteps], (n / kSteps) & 1));
         if (!ok) return;
-        const bool more = !(sh.step[nx % kSteps].flags & kEnd);
-        if (more) load(sh.step[nx % kSteps]);
-        ok = __all_sync(0xffffffffu, wait_for(sh, &sh.pv_done[i][n & 1], (n >> 1) & 1));
+        more = !(sh.step[n % kSteps].flags & kEnd);
+        if (more) load(sh.step[n % kSteps]);
+        ok = __all_sync(0xffffffffu, wait_for(sh, &sh.pv_done[i][last & 1], (last >> 1) & 1));
         if (!ok) return;
         tc::tc_fence_after();
-        const float inv = l > 0.f ? __fdiv_rn(1.f, l) : (l == 0.f ? 0.f : l);
-        // Through the warp's own Q rows (their products are done), so that whole
-        // rows are written: a row's thread puts its columns there 32 at a time
-        // (bf16: all of them, then 16 lanes write a row; fp32: 32 columns, then 8
-        // lanes write a row's 128 bytes).
-        if (slot < 0) {
-#pragma unroll 1
-            for (int part = 0; part < 4; ++part) {
-                uint32_t o[32];
-                tmem_ld32(tO + 32 * part, o);
-                tmem_wait(o);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t v[4];
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * c + 2 * z]) * inv,
-                                                                        __uint_as_float(o[8 * c + 2 * z + 1]) * inv);
-                        v[z] = *reinterpret_cast<const uint32_t*>(&b2);
-                    }
-                    *reinterpret_cast<uint4*>(q_rows + (part >> 1) * kQHalf + lane * 128 + (((4 * (part & 1) + c) ^ (lane & 7)) << 4)) =
-                        make_uint4(v[0], v[1], v[2], v[3]);
-                }
-            }
-            __syncwarp();
-            __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(p.out) + c16 * 8;
-#pragma unroll 2
-            for (int z = 0; z < 16; ++z) {
-                const int r32 = 2 * z + up16;
-                const uint4 v = *reinterpret_cast<const uint4*>(q_rows + (c16 >> 3) * kQHalf + r32 * 128 + (((c16 & 7) ^ (r32 & 7)) << 4));
-                const int64_t to = __shfl_sync(0xffffffffu, own, r32);
-                if (to >= 0) *reinterpret_cast<uint4*>(out + to) = v;
-            }
-        } else {
-            const int64_t at = (int64_t)slot * (2 * kM) + i * kM + (warp & 3) * 32;
-#pragma unroll 1
-            for (int part = 0; part < 4; ++part) {
-                uint32_t o[32];
-                __syncwarp();
-                tmem_ld32(tO + 32 * part, o);
-                tmem_wait(o);
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    *reinterpret_cast<uint4*>(q_rows + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-                        make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-                __syncwarp();
-#pragma unroll 2
-                for (int z = 0; z < 8; ++z) {
-                    const int r32 = 4 * z + (lane >> 3), c = lane & 7;
-                    const uint4 v = *reinterpret_cast<const uint4*>(q_rows + r32 * 128 + ((c ^ (r32 & 7)) << 4));
-                    *reinterpret_cast<uint4*>(p.part + (at + r32) * kHeadDim + 32 * part + 4 * c) = v;
-                }
-            }
-            if (own_on) *reinterpret_cast<float2*>(p.ml + (at + lane) * 2) = make_float2(M, l);
-        }
-        tc::tc_fence_before();
-        __syncwarp();
-        if (!more) return;
-        n = nx;
     }
 }
 
@@ -576,7 +578,7 @@ __device__ __forceinline__ void code_role(Shared& sh, uint8_t* sK, const uint8_t
     for (int n = 0;; ++n) {
         const Step& st = sh.step[n % kSteps];
         if (!wait_for(sh, &sh.info_full[n % kSteps], (n / kSteps) & 1) || (st.flags & kEnd)) return;
-        const int rows = st.there ? st.len - st.key0 : 0;
+        const int rows = st.page >= 0 ? st.len - st.key0 : 0;
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sh.info_empty[n % kSteps]);
         const int bf = n % kBuffers;
@@ -670,7 +672,7 @@ __device__ __forceinline__ void mma_role(Shared& sh, uint32_t aK, uint32_t aQ, u
 }
 
 // =================== the walk ===============================================
-__device__ __forceinline__ void walk_role(const AttnArgs& p, Shared& sh, uint8_t* sKc, int start_h, int64_t left, int lane) {
+__device__ __forceinline__ void walk_role(const AttnArgs& p, Shared& sh, int start_h, int64_t left, int lane) {
     Walk w;
     bool more = w.start(p, start_h, sh.start_b, sh.start_pair, sh.start_off, left);
     if (!more) more = w.next(p);
@@ -716,7 +718,6 @@ __device__ __forceinline__ void walk_role(const AttnArgs& p, Shared& sh, uint8_t
                 lsv = lg2(sv);
                 isv = __fdividef(1.f, sv);
             }
-            const int pg = __shfl_sync(0xffffffffu, page, in);
             ok = __all_sync(0xffffffffu, wait_for(sh, &sh.info_empty[n % kSteps], ((n / kSteps) & 1) ^ 1));
             if (!ok) break;
             if (lane == in) {
@@ -724,7 +725,7 @@ __device__ __forceinline__ void walk_role(const AttnArgs& p, Shared& sh, uint8_t
                 st.flags = i == w.t0 ? kFirst : 0;
                 st.key0 = w.span.step_of(i) * kN;
                 st.left = w.t1 - 1 - i;
-                st.there = page >= 0;
+                st.page = page;
                 st.sk = sk;
                 st.lsv = lsv;
                 st.isv = isv;
@@ -738,19 +739,6 @@ __device__ __forceinline__ void walk_role(const AttnArgs& p, Shared& sh, uint8_t
                 tc::mbar_arrive(&sh.info_full[n % kSteps]);
             }
             __syncwarp();
-            const int64_t at = ((int64_t)max(pg, 0) * p.kv_heads + w.h) * kCodeBytes;
-#pragma unroll 1
-            for (int v = 0; v < 2; ++v) {   // K, then V
-                ok = __all_sync(0xffffffffu, wait_for(sh, &sh.c_empty[v][n & 1], ((n >> 1) & 1) ^ 1));
-                if (!ok) break;
-                if (lane == 0) {
-                    uint64_t* bar = &sh.c_full[v][n & 1];
-                    tc::mbar_arrive_expect_tx(bar, pg >= 0 ? kCodeBytes : 0);
-                    if (pg >= 0) tc::bulk_g2s(sKc + (2 * v + (n & 1)) * kCodeBytes, (v ? p.v : p.k) + at, kCodeBytes, bar);
-                }
-                __syncwarp();
-            }
-            if (!ok) break;
         }
         if (ok) more = w.next(p);
     }
@@ -760,6 +748,30 @@ __device__ __forceinline__ void walk_role(const AttnArgs& p, Shared& sh, uint8_t
             sh.step[n % kSteps].flags = kEnd;
             tc::mbar_arrive(&sh.info_full[n % kSteps]);
         }
+    }
+}
+
+// =================== copies of codes ========================================
+__device__ __forceinline__ void copy_role(const AttnArgs& p, Shared& sh, uint8_t* sKc, int lane) {
+    bool ok = true;
+    for (int n = 0;; ++n) {
+        ok = __all_sync(0xffffffffu, wait_for(sh, &sh.info_full[n % kSteps], (n / kSteps) & 1));
+        if (!ok || (sh.step[n % kSteps].flags & kEnd)) break;
+        const int page = sh.step[n % kSteps].page;
+        const int64_t at = ((int64_t)max(page, 0) * p.kv_heads + sh.step[n % kSteps].h) * kCodeBytes;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sh.info_empty[n % kSteps]);
+#pragma unroll 1
+        for (int v = 0; v < 2 && ok; ++v) {   // K, then V
+            ok = __all_sync(0xffffffffu, wait_for(sh, &sh.c_empty[v][n & 1], ((n >> 1) & 1) ^ 1));
+            if (ok && lane == 0) {
+                uint64_t* bar = &sh.c_full[v][n & 1];
+                tc::mbar_arrive_expect_tx(bar, page >= 0 ? kCodeBytes : 0);
+                if (page >= 0) tc::bulk_g2s(sKc + (2 * v + (n & 1)) * kCodeBytes, (v ? p.v : p.k) + at, kCodeBytes, bar);
+            }
+            __syncwarp();
+        }
+        if (!ok) break;
     }
     if (!ok) {
         // copies may be on their way to readers that have given up: they land
@@ -872,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
     if (t == 0) {
         for (int i = 0; i < kSteps; ++i) {
             tc::mbar_init(&sh.info_full[i], 1);
-            tc::mbar_init(&sh.info_empty[i], kSoftmaxWarps + kCodeWarps);
+            tc::mbar_init(&sh.info_empty[i], kSoftmaxWarps + kCodeWarps + 1);
         }
         for (int i = 0; i < 2; ++i) {
             for (int z = 0; z < kSoftmaxWarps / 2; ++z) tc::mbar_init(&sh.turn[i][z], 1);
@@ -916,7 +928,9 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
         if (warp == kMmaWarp || warp == kMmaWarp + 2) {
             mma_role(sh, uniform(tc::smem_u32(sK)), uniform(tc::smem_u32(sQ)), uniform(tmem), uniform(warp - kMmaWarp) >> 1);
         } else if (warp == kWalkWarp) {
-            walk_role(p, sh, sKc, start_h, left, lane);
+            walk_role(p, sh, start_h, left, lane);
+        } else if (warp == kCopyWarp) {
+            copy_role(p, sh, sKc, lane);
         }
     }
     __syncwarp();
@@ -928,43 +942,52 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
 }
 
 // Pairs that several CTAs share: CTA c's partial 1 begins one, the partials 0
-// of the CTAs after it go on, up to the one that ends it.
+// of the CTAs after it go on, up to the one that ends it.  A warp joins a row at
+// a time, its partials' maxima in the lanes.
 __global__ void __launch_bounds__(256) q8_prompt_join_kernel(const AttnArgs p) {
-    const int cta = blockIdx.x;
+    const int cta = blockIdx.x, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int* m = p.meta + cta * kMeta;
     if (m[1] == 0) return;
-    int n = 0;
-    while (cta + 1 + n < p.ctas) {
-        ++n;
-        if (p.meta[(cta + n) * kMeta] != 0) break;
+    const int b = m[2], h = m[3], pair = m[4];
+    int n = 1;   // partials
+#pragma unroll 1
+    for (int c0 = cta + 1; c0 < p.ctas; c0 += 32) {
+        const uint32_t hit = __ballot_sync(0xffffffffu, c0 + lane < p.ctas && p.meta[(c0 + lane) * kMeta] != 0);
+        n += hit ? __ffs(hit) : 32;
+        if (hit) break;
     }
-    const Seen<kN> r = seen_of<kN>(p, m[2]);
-    const int lane = threadIdx.x & 31;
+    n = min(n, p.ctas - cta);
+    const Seen<kN> r = seen_of<kN>(p, b);
     const int rows = 2 * kM / gridDim.y;
+#pragma unroll 1
     for (int k = threadIdx.x >> 5; k < rows; k += 8) {
-        const int row = blockIdx.y * rows + k;
-        const int q = (row & (kM - 1)) / p.g;
-        const int token = m[4] * 2 * p.tq + (row / kM) * p.tq + q;
+        const int row = blockIdx.y * rows + k, in = row & (kM - 1), q = in / p.g;
+        const int token = pair * 2 * p.tq + (row / kM) * p.tq + q, head = h * p.g + in - q * p.g;
         if (q >= p.tq || token >= r.n) continue;
-        const int head = m[3] * p.g + (row & (kM - 1)) % p.g;
         auto at = [&](int i) { return (int64_t)((cta + i) * 2 + (i == 0 ? 1 : 0)) * (2 * kM) + row; };
-        float M = -INFINITY;
-        for (int i = 0; i <= n; ++i) M = fmaxf(M, p.ml[at(i) * 2]);
-        const float base = M == -INFINITY ? 0.f : M;
-        float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+        float M = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const float2 ml = i0 + lane < n ? *reinterpret_cast<const float2*>(p.ml + at(i0 + lane) * 2) : make_float2(-INFINITY, 0.f);
+            const float now = fmaxf(M, warp_max(ml.x)), base = now == -INFINITY ? 0.f : now;
+            const float f = ex2(ml.x - base), g = ex2(M - base);
+            l = l * g + warp_sum(f * ml.y);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] *= g;
+            M = now;
+            const int c = min(32, n - i0);
 #pragma unroll 4
-        for (int i = 0; i <= n; ++i) {
-            const float2 ml = *reinterpret_cast<const float2*>(p.ml + at(i) * 2);
-            const float4 v = *reinterpret_cast<const float4*>(p.part + at(i) * kHeadDim + 4 * lane);
-            const float f = ex2(ml.x - base);
-            l += f * ml.y;
-            o[0] += f * v.x;
-            o[1] += f * v.y;
-            o[2] += f * v.z;
-            o[3] += f * v.w;
+            for (int i = 0; i < c; ++i) {
+                const float4 v = *reinterpret_cast<const float4*>(p.part + at(i0 + i) * kHeadDim + 4 * lane);
+                const float w = __shfl_sync(0xffffffffu, f, i);
+                o[0] += w * v.x;
+                o[1] += w * v.y;
+                o[2] += w * v.z;
+                o[3] += w * v.w;
+            }
         }
-        const float inv = l > 0.f ? __fdiv_rn(1.f, l) : (l == 0.f ? 0.f : l);
+        const float inv = l > 0.f ? __fdividef(1.f, l) : (l == 0.f ? 0.f : l);
         const __nv_bfloat162 x = __floats2bfloat162_rn(o[0] * inv, o[1] * inv), y = __floats2bfloat162_rn(o[2] * inv, o[3] * inv);
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) +
                                   ((int64_t)(r.first + token) * p.kv_heads * p.g + head) * kHeadDim + 4 * lane) =
@@ -981,7 +1004,7 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.ctas, 8);
+    cfg.gridDim = dim3(a.ctas, 16);
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
