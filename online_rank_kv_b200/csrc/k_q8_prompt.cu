@@ -4,9 +4,10 @@
 // fp16, the key scale multiplies scores, and one exponential
 //     w = 2^(score log2 e + log2 s_v - M)
 // gives the numerator sum w c_v and the denominator sum w / s_v.  M is raised
-// only when a row's maximum has grown by more than 2^8 (weights then stay below
-// 2^15 with the shift of 2^7 that keeps them off fp16's subnormals), so the
-// accumulator in tensor memory is rescaled a few times per row, not per tile.
+// only when a row's maximum has grown past it by more than 2^15, where weights
+// would leave fp16, so the accumulator in tensor memory is rescaled once or
+// twice per row, not per page.  (The largest weight is at least 1; at fp16's
+// smallest steps the others are off by 2^-25 of it.)
 //
 // One CTA per SM holds two tiles of 128 query rows (query tokens x the heads
 // that share a KV head) and goes through the keys in steps of one page:
@@ -57,8 +58,8 @@ constexpr int kSoftmaxWarps = 8, kCodeWarps = 4;
 constexpr int kThreads = 32 * (kSoftmaxWarps + kCodeWarps + 4);
 constexpr int kSoftmaxRegs = 176, kCodeRegs = 80, kOtherRegs = 80;
 constexpr int kMmaWarp = kSoftmaxWarps + kCodeWarps, kWalkWarp = kMmaWarp + 1, kCopyWarp = kMmaWarp + 3;
-constexpr float kShift = 7.f;
-constexpr float kRaise = 8.f;
+constexpr float kRaise = 15.f;
+constexpr int kPolyOf4 = 1;   // of 4 pairs of exponentials, those on the FMA pipe
 // What the start and the end of a pair cost, in steps, where work is split.
 constexpr int kPieceSteps = 8;
 
@@ -84,7 +85,6 @@ struct Shared {
     // Even and odd steps apart: a softmax may be a step ahead of its values'
     // product, and a parity tells only neighbouring phases apart.
     uint64_t pv_done[2][2];
-    uint64_t turn[2][kSoftmaxWarps / 2];
     uint32_t tmem;
     int failed;
     int64_t scan[16];
@@ -145,6 +145,11 @@ __device__ __forceinline__ uint64_t fma2(uint32_t x, uint32_t y, uint64_t a, uin
     asm("{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tfma.rn.f32x2 %0, t, %3, %4;\n\t}" : "=l"(r) : "r"(x), "r"(y), "l"(a), "l"(b));
     return r;
 }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -159,6 +164,25 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
+}
+
+// 2^x of two numbers on the FMA pipe: x = n + f with |f| <= 1/2, a polynomial for
+// 2^f (minimax of the relative error, 2.7e-6; the weight is rounded to 2^-11
+// behind it), n added to its exponent.  Below -126 it stays at 2^-126, which is
+// nothing beside the row's largest weight of 2^-1 or more.
+__device__ __forceinline__ float2 ex2_poly(uint64_t x2) {
+    const float2 x = split(x2);
+    const uint64_t magic = pair(12582912.f, 12582912.f), minus = pair(-12582912.f, -12582912.f), one = pair(-1.f, -1.f);
+    const uint64_t c = pair(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f));
+    const uint64_t r = add2(c, magic), n = add2(r, minus);
+    const uint64_t f = fma2(n, one, c);
+    uint64_t y = fma2(pair(0.009570102207362652f, 0.009570102207362652f), f, pair(0.05591785907745361f, 0.05591785907745361f));
+    y = fma2(y, f, pair(0.240247443318367f, 0.240247443318367f));
+    y = fma2(y, f, pair(0.6931217908859253f, 0.6931217908859253f));
+    y = fma2(y, f, pair(0.9999992847442627f, 0.9999992847442627f));
+    const float2 ry = split(r), yy = split(y);
+    return make_float2(__uint_as_float(__float_as_uint(yy.x) + (__float_as_uint(ry.x) << 23)),
+                       __uint_as_float(__float_as_uint(yy.y) + (__float_as_uint(ry.y) << 23)));
 }
 
 // 32 bytes to global memory: one store where the address allows it.
@@ -422,7 +446,8 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
                                ((key0 + kN - 1 <= wp_min && (p.window == 0 || key0 > wp_max - p.window)) || key0 + kN <= pre);
             // the smallest normal number in place of zero keeps hidden scores at -inf
             float a = fmaxf(rowf * st.sk, 1.17549435e-38f);
-            const float lsv = st.lsv;
+            const float lsv = st.lsv, isv = st.isv;
+            const int left = st.left;
             tmem_wait(*reinterpret_cast<uint32_t(*)[32]>(s));
             tmem_wait(*reinterpret_cast<uint32_t(*)[32]>(s + 32));
             if (MOD) {
@@ -477,21 +502,17 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
                 }
             }
             // ---- weights ----
-            // The two tiles' warps of a scheduler take turns at the exponentials:
-            // each then has them to itself and the other its remaining work.
-            ok = wait_for(sh, &sh.turn[i][warp & 3], i == 0 ? (n & 1) ^ 1 : n & 1);
-            if (!__all_sync(0xffffffffu, ok)) return;
             // One fused multiply-add per weight: x - M with x unrounded, M and
             // M - log2 s_v rounded, off by 2^-24 |M| between pages.  From
             // |M| = 2^10 on, x is rounded like M was first, so that the row's
             // largest key gives exactly x - M = 0.
             const float Mb = M == -INFINITY ? 0.f : M;
-            float b = lsv + (kShift - Mb);
+            float b = lsv - Mb;
             if (__any_sync(0xffffffffu, fabsf(Mb) >= 1024.f)) {
 #pragma unroll
                 for (int e = 0; e < kN; ++e) s[e] = __float_as_uint(fmaf(__uint_as_float(s[e]), a, lsv) - Mb);
                 a = 1.f;
-                b = kShift;
+                b = 0.f;
             }
             const uint64_t aa = pair(a, a), bb = pair(b, b);
             uint64_t sum0 = 0, sum1 = 0;
@@ -500,9 +521,15 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
                 uint32_t o[16];
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                    float2 y = split(fma2(s[32 * c + e], s[32 * c + e + 1], aa, bb));
-                    y.x = ex2(y.x);
-                    y.y = ex2(y.y);
+                    const uint64_t x2 = fma2(s[32 * c + e], s[32 * c + e + 1], aa, bb);
+                    float2 y;
+                    if (((e >> 1) & 3) < kPolyOf4) {
+                        y = ex2_poly(x2);
+                    } else {
+                        y = split(x2);
+                        y.x = ex2(y.x);
+                        y.y = ex2(y.y);
+                    }
                     if (e & 2) sum1 = add2(sum1, pair(y.x, y.y));
                     else sum0 = add2(sum0, pair(y.x, y.y));
                     const __half2 hh = __floats2half2_rn(y.x, y.y);
@@ -510,15 +537,12 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
                 }
                 tc::tmem_st16(tSn + 16 * c, o);
             }
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sh.turn[i ^ 1][warp & 3]);
-            const float2 s2 = split(add2(sum0, sum1));
-            l += (s2.x + s2.y) * st.isv;
-            const int left = st.left;
             tc::tmem_wait_st();
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&sh.p_full[i][n & 1]);
+            const float2 s2 = split(add2(sum0, sum1));   // (nobody waits for these)
+            l += (s2.x + s2.y) * isv;
             if (left == 0) break;
             if (lane == 0) tc::mbar_arrive(&sh.info_empty[n % kSteps]);
             ++n;
@@ -887,7 +911,6 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
             tc::mbar_init(&sh.info_empty[i], kSoftmaxWarps + kCodeWarps + 1);
         }
         for (int i = 0; i < 2; ++i) {
-            for (int z = 0; z < kSoftmaxWarps / 2; ++z) tc::mbar_init(&sh.turn[i][z], 1);
             tc::mbar_init(&sh.q_full[i], kSoftmaxWarps / 2);
             tc::mbar_init(&sh.drain[i], 1);
             for (int z = 0; z < kBuffers; ++z) {
