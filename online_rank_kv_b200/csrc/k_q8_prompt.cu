@@ -431,15 +431,9 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
 
         for (bool first = true;; first = false) {   // steps
             const Step& st = sh.step[n % kSteps];
-            bool ok = wait_for(sh, &sh.info_full[n % kSteps], (n / kSteps) & 1) &&
-                      wait_for(sh, &sh.s_full[i][n & 1], (n >> 1) & 1);
-            ok = __all_sync(0xffffffffu, ok);
+            bool ok = __all_sync(0xffffffffu, wait_for(sh, &sh.info_full[n % kSteps], (n / kSteps) & 1));
             if (!ok) return;
-            tc::tc_fence_after();
             const uint32_t tSn = tS + (n & 1) * kN;
-            uint32_t s[kN];
-            tmem_ld32(tSn, *reinterpret_cast<uint32_t(*)[32]>(s));
-            tmem_ld32(tSn + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
             const int key0 = st.key0;
             const bool there = st.page >= 0;
             const bool clear = there && key0 + kN <= len &&
@@ -448,6 +442,14 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
             float a = fmaxf(rowf * st.sk, 1.17549435e-38f);
             const float lsv = st.lsv, isv = st.isv;
             const int left = st.left;
+            __syncwarp();
+            if (left != 0 && lane == 0) tc::mbar_arrive(&sh.info_empty[n % kSteps]);
+            ok = __all_sync(0xffffffffu, wait_for(sh, &sh.s_full[i][n & 1], (n >> 1) & 1));
+            if (!ok) return;
+            tc::tc_fence_after();
+            uint32_t s[kN];
+            tmem_ld32(tSn, *reinterpret_cast<uint32_t(*)[32]>(s));
+            tmem_ld32(tSn + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
             tmem_wait(*reinterpret_cast<uint32_t(*)[32]>(s));
             tmem_wait(*reinterpret_cast<uint32_t(*)[32]>(s + 32));
             if (MOD) {
@@ -544,7 +546,6 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
             const float2 s2 = split(add2(sum0, sum1));   // (nobody waits for these)
             l += (s2.x + s2.y) * isv;
             if (left == 0) break;
-            if (lane == 0) tc::mbar_arrive(&sh.info_empty[n % kSteps]);
             ++n;
         }
 
