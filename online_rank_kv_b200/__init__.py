@@ -383,6 +383,12 @@ def _int32(device: int, shape, t: torch.Tensor, name: str) -> int:
     return t.data_ptr()
 
 
+def _all_int32(device: int, **tensors) -> None:
+    """Say which of the (shape, tensor) pairs is not what it has to be."""
+    for name, (shape, t) in tensors.items():
+        _int32(device, shape, t, name)
+
+
 def _on_cuda(t: torch.Tensor, name: str) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
@@ -425,14 +431,18 @@ def page_plan(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, free: 
         if tokens is None:
             raise ValueError("tokens (the number of slots) or out is needed")
         out = PagePlan.empty(batch, tokens, lens.device)
-    n = out.slots.shape[0]
-    one = (1,)
-    args = _PlanArgs(batch, width, free.shape[0], n, _int32(dev, (batch,), lens, "lens"),
-                     _int32(dev, (batch,), add, "add"), _int32(dev, (batch, width), table, "table"),
-                     _int32(dev, free.shape, free, "free"), _int32(dev, one, n_free, "n_free"),
-                     _int32(dev, (batch,), out.lens, "out.lens"), _int32(dev, (batch + 1,), out.cu, "out.cu"),
-                     _int32(dev, (n,), out.slots, "out.slots"), _int32(dev, one, out.n_free, "out.n_free"),
-                     _int32(dev, one, out.status, "out.status"))
+    n, pages = out.slots.shape[0], free.shape[0]
+    every = (lens, add, table, free, n_free, out.lens, out.cu, out.slots, out.n_free, out.status)
+    sizes = (batch, batch, batch * width, pages, 1, batch, batch + 1, n, 1, 1)
+    i32 = torch.int32
+    for t, size in zip(every, sizes):
+        if t.dtype is not i32 or t.numel() != size or t.get_device() != dev or not t.is_contiguous():
+            one = (1,)
+            _all_int32(dev, lens=((batch,), lens), add=((batch,), add), table=((batch, width), table),
+                       free=((pages,), free), n_free=(one, n_free), out_lens=((batch,), out.lens),
+                       out_cu=((batch + 1,), out.cu), out_slots=((n,), out.slots), out_n_free=(one, out.n_free),
+                       out_status=(one, out.status))
+    args = _PlanArgs(batch, width, pages, n, *[t.data_ptr() for t in every])
     _launch(dev, LIB.iskv_page_plan, "iskv_page_plan", ctypes.byref(args), stream=stream)
     return out
 
@@ -493,6 +503,8 @@ class Q8Pages:
         """Store rows k, v [n, kv_heads, 128] (any token stride) in the slots
         [n] that ``page_plan`` gave; rows with slot -1 are skipped."""
         dt = self._rows(k, self.kv_heads, "k")
+        if (k.requires_grad or v.requires_grad) and torch.is_grad_enabled():
+            raise ValueError("8-bit pages are forward only: detach k and v")
         if self._rows(v, self.kv_heads, "v") != dt or v.shape != k.shape:
             raise ValueError("k and v must agree in shape and type")
         n = k.shape[0]
@@ -532,13 +544,18 @@ class Q8Pages:
             if len(self._need) < 64:
                 self._need[(heads, max_new, dt)] = need
         ws = q.new_empty(max(need, 0), dtype=torch.uint8)
+        i32 = torch.int32
+        if not (table.dtype is i32 and lens.dtype is i32 and cu.dtype is i32 and cu.numel() == batch + 1
+                and table.get_device() == dev and lens.get_device() == dev and cu.get_device() == dev
+                and table.shape[0] == batch and table.is_contiguous() and lens.is_contiguous() and cu.is_contiguous()):
+            _all_int32(dev, table=((batch, width), table), lens=((batch,), lens), cu=((batch + 1,), cu))
         args = _Q8Attention(batch, width, heads, dt, max_new, window, scale, cap, n, q.stride(0), q.data_ptr(),
-                            out.data_ptr(), _int32(dev, (batch, width), table, "table"),
-                            _int32(dev, (batch,), lens, "lens"), _int32(dev, (batch + 1,), cu, "cu"),
+                            out.data_ptr(), table.data_ptr(), lens.data_ptr(), cu.data_ptr(),
                             None if prefix is None else _int32(dev, (batch,), prefix, "prefix"),
                             None if slopes is None else slopes.data_ptr(), ws.data_ptr(), need, self._status_at)
-        if stream is not None:   # the workspace comes from the current stream's pool
+        if stream is not None:   # both come from the current stream's pool
             ws.record_stream(stream)
+            out.record_stream(stream)
         _launch(dev, LIB.iskv_q8_attention, "iskv_q8_attention", self._ref, ctypes.byref(args), stream=stream)
         return out
 

@@ -58,9 +58,20 @@ int sm_count() {
     return n;
 }
 
-// Row tiles of the split kernel in eights of rows: one where a request's
-// queries of one KV head fit it, else two (which halves the passes over K, V).
-int row_tiles8(int g, int max_new) { return (int64_t)max_new * g <= 8 ? 1 : 2; }
+// Row tiles of the split kernel in eights of rows.  Several tiles of a request
+// read the same keys from L2, and one tile's code is the faster: two pay only for
+// long fp32 prompts (6 requests of 9000 tokens, 3 heads a group: 48 rows 48 us
+// against 51 with two, 192 rows 137 against 106).
+int row_tiles8(int g, int max_new, int dtype) { return dtype == ISKV_F32 && (int64_t)max_new * g > 64 ? 2 : 1; }
+
+// Whether the split kernel gives whole (request, head, tile) items to its CTAs,
+// so that no second launch has to join parts: where requests are very short, or
+// short and many.  (8 KV heads, requests as long as the table; one launch
+// against two: 1 request of 64 tokens 8.9 us against 11.2, of 512 14.8 against
+// 11.9; 64 requests of 512 26.6 against 28.5, ragged ones of up to 1024 36 against 34.)
+bool whole_items(int width, int batch, int kv_heads, int ctas) {
+    return width <= 2 || (width <= 8 && (int64_t)batch * kv_heads >= 2 * (int64_t)ctas);
+}
 
 int64_t rows_floats(int ctas, int tiles8, int dtype) {
     return (int64_t)ctas * q8::rows_parts(tiles8, dtype == ISKV_F32) * 8 * tiles8 * (kHeadDim + 2);
@@ -68,8 +79,11 @@ int64_t rows_floats(int ctas, int tiles8, int dtype) {
 
 int64_t prompt_floats(int ctas) { return (int64_t)ctas * 2 * q8::kPromptRows * (kHeadDim + 2); }
 
-// Query rows per KV head from which a request is a prompt: the tcgen05 kernel
-// works on 256 rows at a time, the split kernel on 8 or 16.
+// Query rows per KV head up to which the split kernel takes a request: the
+// tcgen05 kernel turns every code into an operand whatever the rows, the split
+// kernel goes over the codes once per 8 rows (8 KV heads, 4 heads a group,
+// 16K tokens: 32 rows 39 us in both, 64 rows 57 against 40; 32 requests of 8K
+// tokens: 241 against 272 and 388 against 273).
 constexpr int64_t kPromptMinRows = 32;
 
 bool is_prompt(int g, int max_new, int dtype) { return dtype == ISKV_BF16 && (int64_t)max_new * g > kPromptMinRows; }
@@ -138,7 +152,7 @@ int64_t iskv_q8_workspace(int32_t q_heads, int32_t kv_heads, int64_t tokens, int
     const int ctas = sm_count();
     const int g = q_heads / kv_heads;
     if (is_prompt(g, max_new, dtype)) return prompt_floats(ctas) * 4 + (int64_t)ctas * q8::kMetaBytes;
-    return rows_floats(ctas, row_tiles8(g, max_new), dtype) * 4 + (int64_t)ctas * q8::kMetaBytes;
+    return rows_floats(ctas, row_tiles8(g, max_new, dtype), dtype) * 4 + (int64_t)ctas * q8::kMetaBytes;
 }
 
 int iskv_q8_attention(const iskv_q8_pages* store, const iskv_q8_attention_args* a, void* stream) {
@@ -188,7 +202,7 @@ int iskv_q8_attention(const iskv_q8_pages* store, const iskv_q8_attention_args* 
     p.scale = a->scale;
     p.cap = a->cap;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int tiles8 = row_tiles8(g, a->max_new);
+    const int tiles8 = row_tiles8(g, a->max_new, a->dtype);
     const bool prompt = is_prompt(g, a->max_new, a->dtype);
     p.tq = (prompt ? q8::kPromptRows / 2 : 8 * tiles8) / g;
     p.ctas = sm_count();
@@ -197,6 +211,7 @@ int iskv_q8_attention(const iskv_q8_pages* store, const iskv_q8_attention_args* 
     p.ml = p.part + parts * kHeadDim;
     p.meta = reinterpret_cast<int*>(p.ml + parts * 2);
     p.status = a->status;
+    p.whole = whole_items(a->width, a->batch, store->kv_heads, p.ctas);
     if (prompt)
         return q8::launch_q8_prompt(p, store->code, s) == cudaSuccess ? ISKV_OK : ISKV_ERR_CUDA;
     return q8::launch_q8_rows(p, store->code, a->dtype == ISKV_F32, tiles8, s) == cudaSuccess ? ISKV_OK : ISKV_ERR_CUDA;

@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
     constexpr int kPartsPerCta = 2 * kWarps + 2;
     extern __shared__ uint8_t dyn[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
-    __shared__ int64_t s_scan[kWarps], s_off[kWarps];
+    __shared__ int64_t s_scan[2][kWarps], s_off[kWarps], s_bound[2];
     __shared__ int s_b[kWarps];
     __shared__ Part s_part[kWarps][2];
     __shared__ int s_page[kWarps][kStages];
@@ -233,26 +233,72 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
     // ---- this CTA's and this warp's share of the steps --------------------
     const int chunk = (p.batch + kThreads - 1) / kThreads;
     const int b0 = min(p.batch, t * chunk), b1 = min(p.batch, b0 + chunk);
-    int64_t mine = 0;
+    int64_t mine = 0, items = 0;
 #pragma unroll 1
-    for (int b = b0; b < b1; ++b) mine += units_of(p, b);
-    int64_t incl = mine;
+    for (int b = b0; b < b1; ++b) {
+        const Req q = seen_of<kStepTokens>(p, b);
+        const int64_t n = (int64_t)tiles_of(p, q.n) * p.kv_heads;
+        items += n;
+        mine += n * q.steps;
+    }
+    int64_t incl = mine, incl_items = items;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += u;
+        const int64_t u = __shfl_up_sync(0xffffffffu, incl, o), v = __shfl_up_sync(0xffffffffu, incl_items, o);
+        if (lane >= o) {
+            incl += u;
+            incl_items += v;
+        }
     }
-    if (lane == 31) s_scan[warp] = incl;
+    if (lane == 31) {
+        s_scan[0][warp] = incl;
+        s_scan[1][warp] = incl_items;
+    }
     if (t < kWarps) s_part[t][0].id = s_part[t][1].id = -1;
     __syncthreads();
-    int64_t total = 0, ex = incl - mine;
+    int64_t total = 0, ex = incl - mine, all_items = 0, ex_items = incl_items - items;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) ex += s_scan[w];
-        total += s_scan[w];
+        if (w < warp) {
+            ex += s_scan[0][w];
+            ex_items += s_scan[1][w];
+        }
+        total += s_scan[0][w];
+        all_items += s_scan[1][w];
     }
-    const int64_t per_cta = (total + gridDim.x - 1) / gridDim.x;
-    const int64_t u0 = cta * per_cta, u1 = min(total, u0 + per_cta);
+    int64_t u0, u1;
+    if (p.whole) {   // whole items: nothing is left to be joined
+        const int64_t per_cta = (all_items + gridDim.x - 1) / gridDim.x;
+        if (t < 2) s_bound[t] = total;
+        __syncthreads();
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+            const int64_t want = (cta + k) * per_cta;
+            if (want >= ex_items && want < ex_items + items) {
+                int64_t at_item = ex_items, at = ex;
+                int b = b0;
+#pragma unroll 1
+                for (;; ++b) {
+                    const Req q = seen_of<kStepTokens>(p, b);
+                    const int64_t n = (int64_t)tiles_of(p, q.n) * p.kv_heads;
+                    if (want < at_item + n) {
+                        at += (want - at_item) * q.steps;
+                        break;
+                    }
+                    at_item += n;
+                    at += n * q.steps;
+                }
+                s_bound[k] = at;
+            }
+        }
+        __syncthreads();
+        u0 = s_bound[0];
+        u1 = s_bound[1];
+    } else {
+        const int64_t per_cta = (total + gridDim.x - 1) / gridDim.x;
+        u0 = cta * per_cta;
+        u1 = min(total, u0 + per_cta);
+    }
     if (u0 >= u1) {   // uniform over the CTA
         if (t < kMeta) p.meta[cta * kMeta + t] = 0;
         return;
@@ -768,6 +814,7 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
     q8_rows_kernel<CODE, NT, F32, MOD><<<a.ctas, S::kThreads, kSmemBytes, s>>>(a, map_k, map_v);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    if (a.whole) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.ctas, 8 * NT);
     cfg.blockDim = dim3(256);
@@ -780,16 +827,12 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, q8_join_kernel<NT, F32>, a);
 }
 
-template <int CODE, bool F32, bool MOD>
-cudaError_t by_tiles(const AttnArgs& a, int tiles8, cudaStream_t s) {
-    return tiles8 == 1 ? run<CODE, 1, F32, MOD>(a, s) : run<CODE, 2, F32, MOD>(a, s);
-}
-
 template <int CODE>
 cudaError_t by_type(const AttnArgs& a, bool f32, int tiles8, cudaStream_t s) {
     const bool mod = a.cap > 0.f || a.slopes != nullptr;
-    if (f32) return mod ? by_tiles<CODE, true, true>(a, tiles8, s) : by_tiles<CODE, true, false>(a, tiles8, s);
-    return mod ? by_tiles<CODE, false, true>(a, tiles8, s) : by_tiles<CODE, false, false>(a, tiles8, s);
+    if (!f32) return mod ? run<CODE, 1, false, true>(a, s) : run<CODE, 1, false, false>(a, s);
+    if (tiles8 == 1) return mod ? run<CODE, 1, true, true>(a, s) : run<CODE, 1, true, false>(a, s);
+    return mod ? run<CODE, 2, true, true>(a, s) : run<CODE, 2, true, false>(a, s);
 }
 
 }  // namespace

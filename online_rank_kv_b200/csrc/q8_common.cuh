@@ -64,7 +64,8 @@ struct AttnArgs {
     int window;
     float scale, cap;
     int tq;                    // query tokens per row tile
-    int ctas;                  // CTAs of the split kernel
+    int ctas;                  // CTAs
+    int whole;                 // split kernel: a CTA takes whole items, none is joined across CTAs
     float* part;               // partial results of warps and CTAs
     float* ml;                 // their running maxima and sums
     int* status;               // sticky, or nullptr
