@@ -125,9 +125,10 @@ struct Part {
     int begins, ends; // whether it holds the item's first / last step
 };
 
-__device__ __forceinline__ int64_t units_of(const AttnArgs& p, int b) {
+// A request's items (KV head, row tile) and the steps of each.
+__device__ __forceinline__ int2 shape_of(const AttnArgs& p, int b) {
     const Req r = seen_of<kStepTokens>(p, b);
-    return (int64_t)tiles_of(p, r.n) * r.steps * p.kv_heads;
+    return make_int2(tiles_of(p, r.n) * p.kv_heads, r.steps);
 }
 
 template <bool F32, int N>
@@ -208,7 +209,7 @@ __device__ __forceinline__ bool place_of(const AttnArgs& p, int b, int item, int
 constexpr int kMeta = 4;
 
 template <int CODE, int NT, bool F32, bool MOD>
-__global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(const AttnArgs p, const __grid_constant__ CUtensorMap map_k,
+__global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(const __grid_constant__ AttnArgs p, const __grid_constant__ CUtensorMap map_k,
                                                                                const __grid_constant__ CUtensorMap map_v) {
     constexpr int kWarps = Shape<NT, F32>::kWarps, kThreads = Shape<NT, F32>::kThreads, kStages = Shape<NT, F32>::kStages;
     constexpr int kPartsPerCta = 2 * kWarps + 2;
@@ -217,6 +218,7 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
     __shared__ int64_t s_scan[2][kWarps], s_off[kWarps], s_bound[2];
     __shared__ int s_b[kWarps];
     __shared__ Part s_part[kWarps][2];
+    __shared__ int s_list[2 * kWarps], s_first[2 * kWarps + 1], s_groups;
     __shared__ int s_page[kWarps][kStages];
     __shared__ uint64_t s_full[kWarps][kStages];
     constexpr int R = 8 * NT, PARTS = F32 ? 2 : 1;
@@ -224,6 +226,10 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
     const int r = lane >> 2, q = lane & 3;
     const int cta = blockIdx.x;
     asm volatile("griddepcontrol.launch_dependents;");   // the join may come up; it waits for this grid's end
+    if (t == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k));
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v));
+    }
     if (lane == 0) {
 #pragma unroll
         for (int i = 0; i < kStages; ++i) tc::mbar_init(&s_full[warp][i], 1);
@@ -236,10 +242,9 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
     int64_t mine = 0, items = 0;
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
-        const Req q = seen_of<kStepTokens>(p, b);
-        const int64_t n = (int64_t)tiles_of(p, q.n) * p.kv_heads;
-        items += n;
-        mine += n * q.steps;
+        const int2 n = shape_of(p, b);
+        items += n.x;
+        mine += (int64_t)n.x * n.y;
     }
     int64_t incl = mine, incl_items = items;
 #pragma unroll
@@ -279,14 +284,13 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
                 int b = b0;
 #pragma unroll 1
                 for (;; ++b) {
-                    const Req q = seen_of<kStepTokens>(p, b);
-                    const int64_t n = (int64_t)tiles_of(p, q.n) * p.kv_heads;
-                    if (want < at_item + n) {
-                        at += (want - at_item) * q.steps;
+                    const int2 n = shape_of(p, b);
+                    if (want < at_item + n.x) {
+                        at += (want - at_item) * n.y;
                         break;
                     }
-                    at_item += n;
-                    at += n * q.steps;
+                    at_item += n.x;
+                    at += (int64_t)n.x * n.y;
                 }
                 s_bound[k] = at;
             }
@@ -313,9 +317,9 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
                 int b = b0;
 #pragma unroll 1
                 for (;; ++b) {
-                    const int64_t n = units_of(p, b);
-                    if (off < n) break;
-                    off -= n;
+                    const int2 n = shape_of(p, b);
+                    if (off < (int64_t)n.x * n.y) break;
+                    off -= (int64_t)n.x * n.y;
                 }
                 s_b[w] = b;
                 s_off[w] = off;
@@ -692,22 +696,26 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
     // A group is the parts of one item, which follow each other; (group, row)
     // pairs are dealt to the warps.
     if (t < kMeta) p.meta[cta * kMeta + t] = 0;
-    const int64_t id = lane < 2 * kWarps ? s_part[lane >> 1][lane & 1].id : -1;
-    const uint32_t there = __ballot_sync(0xffffffffu, id >= 0);
-    const uint32_t below = there & ((1u << lane) - 1u);
-    const int64_t id_before = __shfl_sync(0xffffffffu, id, below ? 31 - __clz(below) : 0);
-    const uint32_t heads = __ballot_sync(0xffffffffu, id >= 0 && (below == 0 || id_before != id));
+    if (warp == 0) {
+        const int64_t id = lane < 2 * kWarps ? s_part[lane >> 1][lane & 1].id : -1;
+        const uint32_t there = __ballot_sync(0xffffffffu, id >= 0);
+        const uint32_t below = there & ((1u << lane) - 1u);
+        const int64_t before = __shfl_sync(0xffffffffu, id, below ? 31 - __clz(below) : 0);
+        const bool head = id >= 0 && (below == 0 || before != id);
+        const uint32_t heads = __ballot_sync(0xffffffffu, head);
+        if (id >= 0) s_list[__popc(below)] = lane;
+        if (head) s_first[__popc(heads & ((1u << lane) - 1u))] = __popc(below);
+        if (lane == 0) {
+            s_groups = __popc(heads);
+            s_first[__popc(heads)] = __popc(there);
+        }
+    }
     __syncthreads();
-    const int groups = __popc(heads);
 #pragma unroll 1
-    for (int e = warp; e < groups * R; e += kWarps) {
-        const int grp = e / R, row = e % R;
-        const int first = __fns(heads, 0, grp + 1);
-        const int next = grp + 1 < groups ? (int)__fns(heads, 0, grp + 2) : 32;
-        const uint32_t mine_m = there & (next < 32 ? (1u << next) - 1u : 0xffffffffu) & ~((1u << first) - 1u);
-        const int last_e = 31 - __clz(mine_m);
-        const Part a = s_part[first >> 1][first & 1];
-        const int ends = s_part[last_e >> 1][last_e & 1].ends;
+    for (int e = warp; e < s_groups * R; e += kWarps) {
+        const int grp = e / R, row = e % R, first = s_first[grp], n = s_first[grp + 1] - first;
+        const Part a = s_part[s_list[first] >> 1][s_list[first] & 1];
+        const int ends = s_part[s_list[first + n - 1] >> 1][s_list[first + n - 1] & 1].ends;
         const int b = (int)(a.id >> 32), item = (int)(uint32_t)a.id;
         const bool final = a.begins && ends;
         if (row == 0 && lane == 0 && !final) {
@@ -723,9 +731,9 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
         int64_t out_at;
         if (!place_of(p, b, item, row, &out_at)) continue;
         float M, l, o[4];
-        sum_parts(p, 0, 1, __popc(mine_m),
-                  [&](int k) { return (int64_t)(cta * kPartsPerCta + (int)__fns(mine_m, 0, k + 1)) * R + row; }, lane, M, l, o);
-        put_row<F32>(p, out_at, final ? -1 : (int64_t)(cta * kPartsPerCta + 2 * kWarps + (a.begins ? 1 : 0)) * R + row, M, l, o, lane);
+        const int64_t base = (int64_t)cta * kPartsPerCta * R + row;
+        sum_parts(p, 0, 1, n, [&](int k) { return base + s_list[first + k] * R; }, lane, M, l, o);
+        put_row<F32>(p, out_at, final ? -1 : base + (2 * kWarps + (a.begins ? 1 : 0)) * R, M, l, o, lane);
     }
 }
 
@@ -733,7 +741,7 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
 // 1 begins with the partials 0 of the CTAs after it, up to the one that ends it.
 // Each warp sums some of the partials.
 template <int NT, bool F32>
-__global__ void __launch_bounds__(256) q8_join_kernel(const AttnArgs p) {
+__global__ void __launch_bounds__(256) q8_join_kernel(const __grid_constant__ AttnArgs p) {
     constexpr int R = 8 * NT, kWarps = Shape<NT, F32>::kWarps, kPartsPerCta = 2 * kWarps + 2;
     const int cta = blockIdx.x, row = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     __shared__ float s_ml[8][2], s_o[8][kHeadDim];
