@@ -54,6 +54,23 @@ def rows_of(codes, scale, table_row, length, code):
     return x.transpose(0, 2, 1, 3).reshape(k * ref.PAGE, codes.shape[1], 128)[:length]
 
 
+def step_floor(codes, scale, table_row, length, code, heads, dtype):
+    """What fp16's smallest steps may cost a row's output, [heads, 128].
+
+    A weight w_j is taken relative to M, the largest of score + log2 s_v so far
+    (or at most 2^15 times it): the largest one is at least 1 for the prompt
+    kernel, 2^14 for the other.  fp16 holds it to 2^-25 at worst, so the
+    numerator sum w_j c_j is off by at most 2^-25 sum |c_j|, and the denominator
+    sum w_j / s_j is at least 1 / max s (the largest weight's own term): an
+    error of at most 2^-25 sum |c_j| max s, 2^-39 of it where weights start at
+    2^14 (fp32 queries run on that kernel alone)."""
+    k = -(-length // ref.PAGE)
+    pg = table_row[:k]
+    c = np.abs(ref.decode(codes[pg], code)).transpose(1, 0, 2, 3).reshape(codes.shape[1], -1, 128)[:, :length].sum(1)
+    f = c * scale[pg].max(0).astype(np.float64)[:, None] * 2.0 ** (-25 if dtype == torch.bfloat16 else -39)
+    return np.repeat(f, heads // codes.shape[1], 0)
+
+
 def bound(out, mass, size, dtype, cap=0.0, bias=0.0):
     """Elementwise bound on the error of the kernels' attention.
 

@@ -127,3 +127,20 @@ def test_a_captured_step_replays_with_other_lengths():
             (status, r_lens, cu, slots, r_n)
         np.testing.assert_array_equal(table.cpu().numpy(), r_table)
         np.testing.assert_array_equal(free.cpu().numpy(), r_free)
+
+
+def test_the_largest_batch():
+    rng = np.random.default_rng(40)
+    batch, width = 8192, 3
+    lens = rng.integers(0, 64 * width + 1, batch)
+    add = np.minimum(rng.integers(-1, 9, batch), 64 * width - lens)
+    need = int((-(-lens // 64)).sum())
+    table = np.full((batch, width), -1, dtype=np.int32)
+    order, at = rng.permutation(need + 9000).astype(np.int32), 0
+    for b in range(batch):
+        k = -(-int(lens[b]) // 64)
+        table[b, :k] = order[at:at + k]
+        at += k
+    free = np.concatenate([order[at:], np.zeros(at, dtype=np.int32)])
+    *_, status = _step_both(lens, add, table, free, 9000, int(np.maximum(add, 0).sum()) + 3, in_place=True)
+    assert status == 0

@@ -151,3 +151,53 @@ def test_the_same_call_twice_changes_nothing_more():
         for a, b in zip(before, (pages.k.view(torch.int8), pages.v.view(torch.int8), pages.k_scale, pages.v_scale)):
             assert torch.equal(a, b)
     assert ik.PAGE == 64
+
+
+@pytest.mark.parametrize("code", [ref.INT8, ref.E4M3])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_thousands_of_tokens_in_runs_of_every_length(code, dtype):
+    """Enough tokens that a CTA looks after up to 64 of them: runs that start and
+    end anywhere in its window, cross into the next one, skipped slots between."""
+    rng = np.random.default_rng(31)
+    slots, page = [], 0
+    while len(slots) < 9000:
+        first = int(rng.integers(0, 64))
+        n = int(rng.choice([1, 1, 2, 7, 64 - first, 64]))
+        slots += [page * 64 + r for r in range(first, min(64, first + n))]
+        slots += [-1] * int(rng.integers(0, 3))
+        page += 1
+    x = _rows(len(slots), 2, dtype, seed=32)
+    _check(code, dtype, page + 1, 2, x[0], x[1], slots)
+
+
+def test_quotients_next_to_a_half():
+    """Rows whose quotients by the scale lie within a few ulps of k + 1/2, where a
+    product with the reciprocal rounds to the other side."""
+    top = np.float32(97.31)
+    s = np.float32(top * (np.float32(1) / np.float32(127)))
+    k = np.arange(-126, 126).astype(np.float32) + np.float32(0.5)
+    rows = np.zeros((64, 1, 128), dtype=np.float32)
+    vals = []
+    for d in range(-8, 9):
+        v = (k * s).astype(np.float32)
+        for _ in range(abs(d)):
+            v = np.nextafter(v, np.float32(np.inf if d > 0 else -np.inf)).astype(np.float32)
+        vals.append(v)
+    flat = np.concatenate(vals)[:64 * 128 - 1]
+    rows.reshape(-1)[1:1 + flat.size] = flat
+    rows[0, 0, 0] = top
+    x = torch.from_numpy(rows).cuda()
+    _check(ref.INT8, "f32", 2, 1, x, -x, list(range(64)))
+
+
+def test_a_stream_of_its_own():
+    import online_rank_kv_b200 as ik
+    x = _rows(70, 2, "bf16", seed=33)
+    a, b = ik.Q8Pages(3, 2), ik.Q8Pages(3, 2)
+    slots = torch.arange(70, dtype=torch.int32, device="cuda")
+    a.append(x[0], x[1], slots)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    b.append(x[0], x[1], slots, stream=s)
+    s.synchronize()
+    assert torch.equal(a.k, b.k) and torch.equal(a.v, b.v) and torch.equal(a.k_scale, b.k_scale)

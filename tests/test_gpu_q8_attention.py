@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from oracle import paged_q8 as ref
-from q8_testlib import bound, random_store, rows_of, scattered_table, to_store
+from q8_testlib import bound, random_store, rows_of, scattered_table, step_floor, to_store
 
 pytestmark = pytest.mark.gpu
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
@@ -55,7 +55,8 @@ class Case:
             o, mass, size = ref.attention(q, k, v, scale, cap, slopes, window, 0 if prefix is None else prefix[b])
             bias = 0.0 if slopes is None else 64.0      # beyond it a weight is nothing
             outs.append(o)
-            bounds.append(bound(o, mass, size, self.dtype, cap, bias))
+            floor = step_floor(self.vc, self.vs, self.table[b], n, self.code, self.heads, self.dtype) if n else 0.0
+            bounds.append(bound(o, mass, size, self.dtype, cap, bias) + floor)
             at += m
         return np.concatenate(outs), np.concatenate(bounds)
 
@@ -356,3 +357,93 @@ def test_more_than_two_to_the_31_codes_in_the_pool():
         o, mass, size = ref.attention(q.double().cpu().numpy(), kk, vv, 128 ** -0.5)
         assert (np.abs(out.double().cpu().numpy() - o) <= bound(o, mass, size, torch.bfloat16)).all()
     assert store.status() == 0
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("new", [1, 5, 200])
+@pytest.mark.parametrize("growth", [1.1, 1.7])
+def test_scores_that_grow_along_the_keys(code, new, growth):
+    """Each page's keys are larger than the last one's: the running maximum is
+    raised again and again, by little and by much."""
+    c = Case([900], [new], 2, 4, code, seed=21, gain=0.03)
+    for j in range(15):
+        c.ks[c.table[0, j]] = np.float32(2.0 ** -9 * growth ** j)
+    c.check()
+
+
+@pytest.mark.parametrize("new", [1, 200])
+def test_scores_far_below_the_first_page(new):
+    """A first page far above all others: their weights end below every range."""
+    c = Case([900], [new], 2, 4, ref.INT8, seed=22)
+    c.ks[c.table[0, 0]] *= np.float32(200.0)
+    c.check()
+
+
+@pytest.mark.parametrize("new", [1, 9, 40])
+def test_many_requests_at_the_batch_limit(new):
+    rng = np.random.default_rng(23)
+    n = 8192 if new == 1 else 300
+    lens = rng.integers(0 if new == 1 else new, 90, n).tolist()
+    news = [min(k, new) for k in lens] if new == 1 else rng.integers(0, new + 1, n).tolist()
+    Case(lens, news, 1, 2, ref.E4M3, seed=24).check()
+
+
+@pytest.mark.parametrize("dtype,new", [("bf16", 1), ("f32", 6), ("bf16", 150)])
+def test_buffers_that_are_16_byte_aligned_and_no_more(dtype, new):
+    import ctypes
+    import online_rank_kv_b200 as ik
+    c = Case([700, 333], [new, new], 2, 4, ref.INT8, dtype, seed=25)
+    n, per16 = c.q.shape[0], 16 // c.q.element_size()
+    out = torch.zeros(c.q.numel() + per16, dtype=c.dtype, device="cuda")[per16:].view(c.q.shape)
+    q = torch.zeros(c.q.numel() + per16, dtype=c.dtype, device="cuda")[per16:].view(c.q.shape).copy_(c.q)
+    dt = ik.BF16 if dtype == "bf16" else ik.F32
+    need = ik.LIB.iskv_q8_workspace(c.heads, 2, n, new, dt)
+    ws = torch.empty(need + 16, dtype=torch.uint8, device="cuda")[16:]
+    assert out.data_ptr() % 32 == 16 and ws.data_ptr() % 32 == 16
+    table = torch.from_numpy(c.table.copy()).cuda()
+    lens = torch.tensor(c.lens, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, new, 2 * new], dtype=torch.int32, device="cuda")
+    store = c.store()
+    a = ik._Q8Attention(2, table.shape[1], c.heads, dt, new, 0, 128 ** -0.5, 0.0, n, q.stride(0), q.data_ptr(),
+                        out.data_ptr(), table.data_ptr(), lens.data_ptr(), cu.data_ptr(), None, None, ws.data_ptr(), need,
+                        None)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert ik.LIB.iskv_q8_attention(store._ref, ctypes.byref(a), stream) == 0
+    w, tol = c.want()
+    assert (np.abs(out.double().cpu().numpy() - w) <= tol).all()
+    a.workspace_bytes = need - 1
+    assert ik.LIB.iskv_q8_attention(store._ref, ctypes.byref(a), stream) == -2
+    host = (ctypes.c_int32 * 4)()
+    a.workspace_bytes, a.lens = need, ctypes.addressof(host)
+    assert ik.LIB.iskv_q8_attention(store._ref, ctypes.byref(a), stream) == -1     # host memory
+
+
+@pytest.mark.parametrize("new", [1, 150])
+def test_a_stream_of_its_own_and_another_scale(new):
+    c = Case([700, 333], [new, new], 2, 4, ref.INT8, seed=26)
+    c.store()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = c.run(stream=s, scale=0.05)
+    s.synchronize()
+    w, tol = c.want(scale=0.05)
+    assert (np.abs(got.double().cpu().numpy() - w) <= tol).all()
+
+
+@pytest.mark.parametrize("max_new", [1, 300])
+def test_no_queries_and_no_requests(max_new):
+    import online_rank_kv_b200 as ik
+    store = ik.Q8Pages(2, 2)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.zeros(0, 8, 128, dtype=torch.bfloat16, device="cuda")
+    out = store.attention(q, torch.zeros(3, 2, **i32), torch.zeros(3, **i32), torch.zeros(4, **i32), max_new=max_new)
+    assert out.shape == (0, 8, 128)
+    q = torch.zeros(5, 8, 128, dtype=torch.bfloat16, device="cuda")
+    given = torch.full_like(q, 3.0)
+    out = store.attention(q, torch.zeros(0, 2, **i32), torch.zeros(0, **i32), torch.zeros(1, **i32), max_new=max_new, out=given)
+    assert (out == 3.0).all()
+    # requests without queries beside slots of a padded batch
+    out = store.attention(q, torch.zeros(3, 2, **i32), torch.full((3,), 100, **i32), torch.zeros(4, **i32), max_new=max_new,
+                          out=given)
+    torch.cuda.synchronize()
+    assert (out == 3.0).all() and store.status() == 0
