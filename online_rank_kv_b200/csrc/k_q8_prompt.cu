@@ -61,7 +61,7 @@ constexpr int kMmaWarp = kSoftmaxWarps + kCodeWarps, kWalkWarp = kMmaWarp + 1, k
 constexpr float kRaise = 15.f;
 constexpr int kPolyOf4 = 1;   // of 4 pairs of exponentials, those on the FMA pipe
 // What the start and the end of a pair cost, in steps, where work is split.
-constexpr int kPieceSteps = 8;
+constexpr int kPieceSteps = 6;
 
 // One step, as the walking warp describes it.
 constexpr int kFirst = 1, kEnd = 2;     // of a piece; of the work
@@ -428,6 +428,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
         const int wp_min = __reduce_min_sync(0xffffffffu, pos), wp_max = __reduce_max_sync(0xffffffffu, pos);
         M = -INFINITY;
         l = 0.f;
+        bool huge = false;   // some row of the warp has |M| >= 2^10
 
         for (bool first = true;; first = false) {   // steps
             const Step& st = sh.step[n % kSteps];
@@ -487,6 +488,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
             if (__any_sync(0xffffffffu, raise)) {
                 const float f = raise && M > -INFINITY ? ex2(M - now) : 1.f;
                 if (raise) M = now;
+                huge = __any_sync(0xffffffffu, M > -INFINITY && fabsf(M) >= 1024.f);
                 l *= f;
                 if (!first) {   // the accumulator holds earlier steps
                     ok = __all_sync(0xffffffffu, wait_for(sh, &sh.pv_done[i][(n - 1) & 1], ((n - 1) >> 1) & 1));
@@ -510,7 +512,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
             // largest key gives exactly x - M = 0.
             const float Mb = M == -INFINITY ? 0.f : M;
             float b = lsv - Mb;
-            if (__any_sync(0xffffffffu, fabsf(Mb) >= 1024.f)) {
+            if (huge) {
 #pragma unroll
                 for (int e = 0; e < kN; ++e) s[e] = __float_as_uint(fmaf(__uint_as_float(s[e]), a, lsv) - Mb);
                 a = 1.f;
