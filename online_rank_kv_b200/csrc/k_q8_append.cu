@@ -37,6 +37,15 @@ struct Raw<float> {
         b = __ldg(reinterpret_cast<const float4*>(p) + 1);
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    // the largest magnitude's fp32 bits: they order like the values, with
+    // infinity and NaN above all numbers
+    __device__ __forceinline__ uint32_t top() const {
+        const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+        return m;
+    }
     __device__ __forceinline__ void get(float (&v)[8]) const {
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
         v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
@@ -47,6 +56,11 @@ struct Raw<__nv_bfloat16> {
     uint4 a;
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
     __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ uint32_t top() const {
+        const uint32_t k = 0x7fff7fffu;
+        const uint32_t m = __vmaxu2(__vmaxu2(a.x & k, a.y & k), __vmaxu2(a.z & k, a.w & k));
+        return max(m & 0xffff0000u, m << 16);
+    }
     __device__ __forceinline__ void get(float (&v)[8]) const {
         const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -69,12 +83,10 @@ __device__ __forceinline__ float scale_of(float top) {
     return __uint_as_float((uint32_t)e << 23);
 }
 
-// Codes of 8 quotients x / s, s > 0, with inv = 1 / s; not finite ones are zeros.
+// Codes of 8 quotients x / s, s > 0, with inv = 1 / s.
 constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: adding it rounds to a whole number, half to even
 template <int CODE>
 __device__ __forceinline__ uint2 code8(float (&v)[8], float s, float inv) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = fabsf(v[e]) < INFINITY ? v[e] : 0.f;
     if constexpr (CODE == ISKV_CODE_INT8) {
         float y[8], near = 0.f;
 #pragma unroll
@@ -190,32 +202,38 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 5) q8_append_ke
         // 16 threads per row, 8 rows per pass
         const int col = (t & 15) * 8;
         Raw<T> v[kPasses];
-        float top = 0.f;
-        bool bad = false;
 #pragma unroll
         for (int s = 0; s < kPasses; ++s) {
             const int r = s * (kThreads / 16) + (t >> 4);
             if (r < n) v[s].load(x + (i + r) * stride + head * kHeadDim + col);
             else v[s].zero();
         }
+        uint32_t bits = 0;
 #pragma unroll
-        for (int s = 0; s < kPasses; ++s) {
-            float u[8];
-            v[s].get(u);
+        for (int s = 0; s < kPasses; ++s) bits = max(bits, v[s].top());
+        if (bits >= 0x7f800000u) {   // infinities and NaN are stored as zeros and do not count
+            if (p.status) atomicMin(p.status, ISKV_ERR_RANGE);
+            float m = 0.f;
+#pragma unroll 1
+            for (int s = 0; s < kPasses; ++s) {
+                const int r = s * (kThreads / 16) + (t >> 4);
+                if (r >= n) continue;
+                Raw<T> w;
+                w.load(x + (i + r) * stride + head * kHeadDim + col);
+                float u[8];
+                w.get(u);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float m = fabsf(u[e]);
-                bad = bad || !(m < INFINITY);   // infinities and NaN are stored as zeros
-                top = fmaxf(top, m < INFINITY ? m : 0.f);
+                for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(u[e]) < INFINITY ? fabsf(u[e]) : 0.f);
             }
+            bits = __float_as_uint(m) | 0x80000000u;   // (finite: the top bit marks the thread)
         }
-        if (bad && p.status) atomicMin(p.status, ISKV_ERR_RANGE);
-        top = warp_max(top);
-        if (lane == 0) s_top[warp] = top;
+        const bool dirty = bits >> 31;
+        const uint32_t most = __reduce_max_sync(0xffffffffu, bits & 0x7fffffffu);
+        if (lane == 0) s_top[warp] = __uint_as_float(most);
         const int64_t block = (slot / kPage) * p.kv_heads + head;
         const float before = row0 > 0 ? scale[block] : 0.f;
         __syncthreads();   // every thread has read the old scale
-        top = s_top[0];
+        float top = s_top[0];
 #pragma unroll
         for (int w = 1; w < kThreads / 32; ++w) top = fmaxf(top, s_top[w]);
         const float now = fmaxf(before, scale_of<CODE>(top));
@@ -244,6 +262,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 5) q8_append_ke
             if (now > 0.f) {
                 float u[8];
                 v[s].get(u);
+                if (dirty) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) u[e] = fabsf(u[e]) < INFINITY ? u[e] : 0.f;
+                }
                 c = code8<CODE>(u, now, inv);
             }
             *reinterpret_cast<uint2*>(base + (row0 + r) * kHeadDim + col) = c;
