@@ -432,7 +432,10 @@ ISKV_API int iskv_page_plan(const iskv_page_plan_args* args, void* stream);
  *     2^e with the block's largest |x| <= 448 * 2^e, code = x / 2^e rounded
  *     half to even.
  * A block whose largest value is below 2^-64 is stored as zeros, scale 0.
- * Scales are 0 or in [2^-72, 2^122]; e4m3 codes are not NaN (iskv_q8_append
+ * Scales are 0 or in [2^-72, 2^122], and the value scales of the pages that one
+ * query sees lie within a factor of 2^100 of each other (attention takes a key's
+ * weight and its value scale in one fp32 number: pages further below the largest
+ * may count as nothing); e4m3 codes are not NaN (iskv_q8_append
  * writes nothing else).                                                     */
 #define ISKV_CODE_INT8 0
 #define ISKV_CODE_E4M3 1

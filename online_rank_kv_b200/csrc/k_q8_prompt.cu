@@ -34,10 +34,17 @@
 // and short chunks on long caches all fill the GPU; a pair that crosses CTAs is
 // joined from its partial sums by a second kernel.
 //
-// Bounds per 128 keys and pair (148 SMs): 2048 cycles of MMA at the nominal
-// rate (64 per instruction of 128 x 128 x 16), about 3000 at the rate that the
-// chip holds under its power limit; 2048 cycles of exponentials (16 per SM and
-// clock).
+// What bounds it: a page and pair of tiles is 1024 cycles of MMA at the nominal
+// rate, about 1400 as issued here (64-column score products wait for Q in shared
+// memory), and 1024 cycles of exponentials (16 per SM and clock) less the quarter
+// on the FMA pipe.  It takes about 2000: the two tiles' chains -- weights handed
+// over, their values' product, the scores after next, softmax -- do not overlap
+// fully.  Whatever lengthens the way from scores to weights shows at once: the
+// sums taken behind the hand-over instead of before it were 683 -> 574 us of an
+// 8192-token prompt (32 query, 8 KV heads).  That prompt takes 553 us: 994
+// TFLOP/s, 60 % of the measured matrix rate; 596 us in long runs, at the power
+// limit.  Tried and slower: 128-column scores in one buffer (726 against 659),
+// no maximum but a check of the sums (645 against 558).
 #include "q8_common.cuh"
 #include "tc_util.cuh"
 
@@ -58,9 +65,14 @@ constexpr int kSoftmaxWarps = 8, kCodeWarps = 4;
 constexpr int kThreads = 32 * (kSoftmaxWarps + kCodeWarps + 4);
 constexpr int kSoftmaxRegs = 176, kCodeRegs = 80, kOtherRegs = 80;
 constexpr int kMmaWarp = kSoftmaxWarps + kCodeWarps, kWalkWarp = kMmaWarp + 1, kCopyWarp = kMmaWarp + 3;
+// How far (in powers of two) a row's maximum may pass M before M is raised: the
+// weights then reach 2^15.
 constexpr float kRaise = 15.f;
-constexpr int kPolyOf4 = 1;   // of 4 pairs of exponentials, those on the FMA pipe
-// What the start and the end of a pair cost, in steps, where work is split.
+// Of 4 pairs of exponentials, those taken on the FMA pipe (8192-token prompt:
+// none 590 us, one of eight 568, one of four 558, two 607).
+constexpr int kPolyOf4 = 1;
+// What the start and the end of a pair cost, in steps, where work is split
+// (8192-token prompt: 4 571 us, 6 553, 8 558, 12 570).
 constexpr int kPieceSteps = 6;
 
 // One step, as the walking warp describes it.
@@ -155,6 +167,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+// Sums of weights: what is below 2^-126 counts as nothing (ex2_poly's hidden keys).
+__device__ __forceinline__ uint64_t sum2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.ftz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ float2 split(uint64_t a) {
     float2 r;
     asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
@@ -168,8 +186,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // 2^x of two numbers on the FMA pipe: x = n + f with |f| <= 1/2, a polynomial for
 // 2^f (minimax of the relative error, 2.7e-6; the weight is rounded to 2^-11
-// behind it), n added to its exponent.  Below -126 it stays at 2^-126, which is
-// nothing beside the row's largest weight of 2^-1 or more.
+// behind it), n added to its exponent.  x is at most kRaise; from -126 down
+// (hidden keys: -inf) the result is just below 2^-126, which fp16 drops and sum2
+// takes as nothing.
 __device__ __forceinline__ float2 ex2_poly(uint64_t x2) {
     const float2 x = split(x2);
     const uint64_t magic = pair(12582912.f, 12582912.f), minus = pair(-12582912.f, -12582912.f), one = pair(-1.f, -1.f);
@@ -534,8 +553,8 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
                         y.x = ex2(y.x);
                         y.y = ex2(y.y);
                     }
-                    if (e & 2) sum1 = add2(sum1, pair(y.x, y.y));
-                    else sum0 = add2(sum0, pair(y.x, y.y));
+                    if (e & 2) sum1 = sum2(sum1, pair(y.x, y.y));
+                    else sum0 = sum2(sum0, pair(y.x, y.y));
                     const __half2 hh = __floats2half2_rn(y.x, y.y);
                     o[e >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
                 }
@@ -545,7 +564,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&sh.p_full[i][n & 1]);
-            const float2 s2 = split(add2(sum0, sum1));   // (nobody waits for these)
+            const float2 s2 = split(sum2(sum0, sum1));   // (nobody waits for these)
             l += (s2.x + s2.y) * isv;
             if (left == 0) break;
             ++n;

@@ -187,6 +187,26 @@ def test_queries_in_front_of_the_stored_tokens_get_zeros(new, prefix):
         assert (got[:new - 2] == 0).all()
 
 
+@pytest.mark.parametrize("scale", [2.0 ** -60, 2.0 ** 60, 2.0 ** 110])
+@pytest.mark.parametrize("new", [4, 200])
+def test_empty_rows_are_zeros_whatever_the_scales(new, scale):
+    c = Case([2, 90], [new, new], 2, 4, ref.INT8, seed=27)
+    c.vs *= np.float32(scale)
+    got = c.run().double().cpu().numpy()
+    assert (got[:new - 2] == 0).all() and np.isfinite(got).all()
+
+
+@pytest.mark.parametrize("new", [1, 200])
+def test_hidden_pages_of_tiny_values_beside_huge_ones(new):
+    """Value scales 98 powers of two apart (a query's pages may be up to 2^100
+    apart): what a row does not see must not count, however large 1 / scale is,
+    and what it sees counts in the denominator with its weight."""
+    c = Case([700], [new], 2, 4, ref.INT8, seed=28)
+    c.vs[:] = np.float32(2.0 ** 60)
+    c.vs[c.table[0, ::2]] = np.float32(2.0 ** -38)
+    c.check(window=70)
+
+
 @pytest.mark.parametrize("new", [1, 3, 130])
 def test_requests_that_hold_nothing_get_zeros(new):
     c = Case([0, 200, 0], [new, new, new], 2, 4, ref.INT8, seed=9, extra_width=1)
