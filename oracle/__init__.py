@@ -16,6 +16,10 @@ Sources (web pages, cited by title and section):
     covariance route to the batch SVD, used only by the tests as an independent
     cross-check.
 
+``paged_q8`` is the reference of the paged 8-bit cache of exact tokens (page
+tables, coded writes, ragged attention); it comes from the header's definitions,
+not from a page.
+
 Parity status per function is stated in each docstring ("pinned by ..." or
 "parity unpinned").
 """
