@@ -42,6 +42,8 @@ __device__ __forceinline__ int last_at_most(const int* v, int n, int x) {
 
 __global__ void __launch_bounds__(kThreads) page_plan_kernel(const iskv_page_plan_args a) {
     extern __shared__ int sh[];
+    let_next();
+    after_previous();
     __shared__ long long warp_sum[3][32], s_total[3];
     const int B = a.batch;
     int* s_len = sh;                  // [B]
@@ -205,19 +207,7 @@ cudaError_t launch_page_plan(const iskv_page_plan_args& a, cudaStream_t s) {
     // four slots per thread, up to what a portable cluster holds
     int ctas = 1;
     while (ctas < 8 && (int64_t)ctas * 4 * kThreads < a.tokens) ctas *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = ctas;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, page_plan_kernel, a);
+    return launch_early(page_plan_kernel, dim3(ctas), kThreads, smem, s, ctas, a);
 }
 
 }  // namespace q8

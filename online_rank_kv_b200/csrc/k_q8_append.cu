@@ -152,6 +152,8 @@ __device__ __forceinline__ void decode4(uint32_t x, float (&v)[4]) {
 
 template <int CODE, typename T>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 5) q8_append_kernel(const AppendArgs p) {
+    let_next();
+    after_previous();
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int head = blockIdx.y, which = blockIdx.z;
     const T* x = static_cast<const T*>(which ? p.x[1] : p.x[0]);
@@ -283,13 +285,12 @@ cudaError_t launch_q8_append(const AppendArgs& a, int code, int dtype, cudaStrea
     if (a.n == 0) return cudaSuccess;
     const dim3 grid((unsigned)((a.n + a.window - 1) / a.window), a.kv_heads, 2);
     if (code == ISKV_CODE_INT8) {
-        if (dtype == ISKV_F32) q8_append_kernel<ISKV_CODE_INT8, float><<<grid, kThreads, 0, s>>>(a);
-        else q8_append_kernel<ISKV_CODE_INT8, __nv_bfloat16><<<grid, kThreads, 0, s>>>(a);
+        if (dtype == ISKV_F32) return launch_early(q8_append_kernel<ISKV_CODE_INT8, float>, grid, kThreads, 0, s, 0, a);
+        else return launch_early(q8_append_kernel<ISKV_CODE_INT8, __nv_bfloat16>, grid, kThreads, 0, s, 0, a);
     } else {
-        if (dtype == ISKV_F32) q8_append_kernel<ISKV_CODE_E4M3, float><<<grid, kThreads, 0, s>>>(a);
-        else q8_append_kernel<ISKV_CODE_E4M3, __nv_bfloat16><<<grid, kThreads, 0, s>>>(a);
+        if (dtype == ISKV_F32) return launch_early(q8_append_kernel<ISKV_CODE_E4M3, float>, grid, kThreads, 0, s, 0, a);
+        else return launch_early(q8_append_kernel<ISKV_CODE_E4M3, __nv_bfloat16>, grid, kThreads, 0, s, 0, a);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace q8

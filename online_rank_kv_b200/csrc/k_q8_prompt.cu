@@ -834,7 +834,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int cta = blockIdx.x;
-    asm volatile("griddepcontrol.launch_dependents;");   // the join may come up; it waits for this grid's end
+    let_next();
+    after_previous();
 
     // ---- this CTA's range -------------------------------------------------
     // pairs of query tiles up to each request, then cost up to each pair
@@ -991,7 +992,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
 // a time, its partials' maxima in the lanes.
 __global__ void __launch_bounds__(256) q8_prompt_join_kernel(const AttnArgs p) {
     const int cta = blockIdx.x, lane = threadIdx.x & 31;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    let_next();
+    after_previous();
     const int* m = p.meta + cta * kMeta;
     if (m[1] == 0) return;
     const int b = m[2], h = m[3], pair = m[4];
@@ -1045,19 +1047,9 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
     static SmemOnce once;
     cudaError_t e = once.set(q8_prompt_kernel<CODE, MOD>, kSmemBytes);
     if (e != cudaSuccess) return e;
-    q8_prompt_kernel<CODE, MOD><<<a.ctas, kThreads, kSmemBytes, s>>>(a);
-    e = cudaGetLastError();
+    e = launch_early(q8_prompt_kernel<CODE, MOD>, dim3(a.ctas), kThreads, kSmemBytes, s, 0, a);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.ctas, 16);
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, q8_prompt_join_kernel, a);
+    return launch_early(q8_prompt_join_kernel, dim3(a.ctas, 16), 256, 0, s, 0, a);
 }
 
 }  // namespace

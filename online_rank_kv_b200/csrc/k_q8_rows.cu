@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int r = lane >> 2, q = lane & 3;
     const int cta = blockIdx.x;
-    asm volatile("griddepcontrol.launch_dependents;");   // the join may come up; it waits for this grid's end
+    let_next();
     if (t == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k));
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v));
@@ -242,6 +242,7 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
         for (int i = 0; i < kStages; ++i) tc::mbar_init(&s_full[warp][i], 1);
         tc::fence_mbar_init();
     }
+    after_previous();
 
     // ---- this CTA's and this warp's share of the steps --------------------
     const int chunk = (p.batch + kThreads - 1) / kThreads;
@@ -752,7 +753,8 @@ __global__ void __launch_bounds__(256) q8_join_kernel(const __grid_constant__ At
     constexpr int R = 8 * NT, kWarps = Shape<NT, F32>::kWarps, kPartsPerCta = 2 * kWarps + 2;
     const int cta = blockIdx.x, row = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     __shared__ float s_ml[8][2], s_o[8][kHeadDim];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    let_next();
+    after_previous();
     const int4 m = *reinterpret_cast<const int4*>(p.meta + cta * kMeta);
     if (m.y == 0) return;
     int64_t out_at;
@@ -826,20 +828,9 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     CUtensorMap map_k, map_v;
     if (!tensor_map(a, a.k, &map_k) || !tensor_map(a, a.v, &map_v)) return cudaErrorInvalidValue;
-    q8_rows_kernel<CODE, NT, F32, MOD><<<a.ctas, S::kThreads, kSmemBytes, s>>>(a, map_k, map_v);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    if (a.whole) return cudaSuccess;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.ctas, 8 * NT);
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, q8_join_kernel<NT, F32>, a);
+    e = launch_early(q8_rows_kernel<CODE, NT, F32, MOD>, dim3(a.ctas), S::kThreads, kSmemBytes, s, 0, a, map_k, map_v);
+    if (e != cudaSuccess || a.whole) return e;
+    return launch_early(q8_join_kernel<NT, F32>, dim3(a.ctas, 8 * NT), 256, 0, s, 0, a);
 }
 
 template <int CODE>

@@ -35,6 +35,33 @@ struct SmemOnce {
     }
 };
 
+// Launches a kernel that may come up while the one before it in the stream ends.
+// It calls after_previous() before it touches memory, which waits for that
+// kernel's end and its writes; kernels call let_next() at once, so that what
+// follows them need not wait for its own launch. A page plan and eight layers of
+// append and attention, 1000 keys a request: batch 1 119 -> 113 us as a graph,
+// batch 64 394 -> 364 us launched one by one (387 -> 386 as a graph).
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, int cluster, const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 0 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 struct AppendArgs {
     const void* x[2];          // k, v
     int64_t stride[2];         // elements from token to token

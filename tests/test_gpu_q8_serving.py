@@ -182,3 +182,75 @@ def test_other_gpus_tensors_are_refused_by_the_binding():
         store.attention(torch.zeros(1, 9 * KV, 128, device="cuda"), _i32([[0]]), _i32([1]), _i32([0, 1]), max_new=1)
     with pytest.raises(ValueError):
         store.attention(q.detach(), _i32([[0]]), _i32([1, 2]), _i32([0, 1]), max_new=1)
+
+
+def test_calls_follow_one_another_without_a_gap():
+    """Many short calls in a row, each reading what the one before wrote, with
+    copies and a second stream between them, captured and replayed: the same
+    bits as with a synchronize after each call."""
+    import online_rank_kv_b200 as ik
+    batch, steps = 3, 12
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    qkv = torch.randn(steps, batch, HEADS + 2 * KV, 128, generator=gen, device="cuda").bfloat16()
+
+    def run(layer, plan, state, outs, sync, side):
+        table, free = state
+        plan.lens.zero_()
+        plan.n_free.fill_(PAGES)
+        free.copy_(torch.arange(PAGES, dtype=torch.int32, device="cuda"))
+        add = torch.ones(batch, dtype=torch.int32, device="cuda")
+        x = torch.empty_like(qkv[0])
+        for i in range(steps):
+            x.copy_(qkv[i])
+            q, k, v = x[:, :HEADS], x[:, HEADS:HEADS + KV], x[:, HEADS + KV:]
+            ik.page_plan(plan.lens, add, table, free, plan.n_free, out=plan)
+            sync()
+            layer.append(k, v, plan.slots)
+            sync()
+            if side is not None and i % 3 == 1:
+                here = torch.cuda.current_stream()
+                side.wait_stream(here)
+                with torch.cuda.stream(side):
+                    layer.attention(q, table, plan.lens, plan.cu, max_new=1, out=outs[i])
+                here.wait_stream(side)
+            else:
+                layer.attention(q, table, plan.lens, plan.cu, max_new=1, out=outs[i])
+            sync()
+            # what the attention answered is part of the next step's input
+            if i + 1 < steps:
+                qkv_next = outs[i][:, :KV] * 0.25
+                layer.append(qkv_next, qkv_next, plan.slots)
+                sync()
+
+    def fresh():
+        plan = ik.PagePlan.empty(batch, batch)
+        state = (_i32(np.full((batch, WIDTH), -1)), _i32(np.arange(PAGES)))
+        outs = [torch.zeros(batch, HEADS, 128, dtype=torch.bfloat16, device="cuda") for _ in range(steps)]
+        return ik.Q8Pages(PAGES, KV, ik.CODE_E4M3), plan, state, outs
+
+    want = fresh()
+    run(*want, torch.cuda.synchronize, None)
+    side = torch.cuda.Stream()
+    eager = fresh()
+    run(*eager, lambda: None, side)
+    torch.cuda.synchronize()
+    captured = fresh()
+    run(*captured, torch.cuda.synchronize, side)      # buffers in place
+    captured[0].k.zero_()
+    captured[0].v.zero_()
+    captured[0].k_scale.zero_()
+    captured[0].v_scale.zero_()
+    captured[2][0].fill_(-1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(*captured, lambda: None, side)
+    for o in captured[3]:
+        o.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    for got in (eager, captured):
+        for a, b in zip(got[3], want[3]):
+            assert torch.equal(a, b)
+        assert torch.equal(got[0].k.view(torch.uint8), want[0].k.view(torch.uint8))
+        assert torch.equal(got[0].v_scale, want[0].v_scale)
+        assert got[0].status() == 0
