@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const iskv_page_pla
     cg::this_cluster().sync();   // every CTA has read lens and n_free
 
     const int gt = blockIdx.x * kThreads + t, step = gridDim.x * kThreads;
+    const uint32_t n_slots = (uint32_t)a.tokens;   // (up to 2^31 - 1: steps past it stay within 32 bits without a sign)
     if (gt == 0) {
         *a.status = bad_arg ? ISKV_ERR_INVALID_ARG : bad_cap ? ISKV_ERR_CAPACITY : ISKV_OK;
         *a.n_free_out = (int)(refused ? n_free : top - total[1]);
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const iskv_page_pla
     if (refused) {
         for (int b = gt; b < B; b += step) a.lens_out[b] = s_len[b];
         for (int b = gt; b <= B; b += step) a.cu[b] = 0;
-        for (int i = gt; i < a.tokens; i += step) a.slots[i] = -1;
+        for (uint32_t i = gt; i < n_slots; i += step) a.slots[i] = -1;
         return;
     }
     const int nf = (int)n_free, n1 = (int)top;
@@ -166,11 +167,12 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const iskv_page_pla
     // where there are many slots, a thread's four follow each other: one search,
     // and mostly one page
     const int per = a.tokens <= step ? 1 : 4;
-    for (int i0 = per * gt; i0 < a.tokens; i0 += per * step) {
-        int b = i0 < added ? last_at_most(s_cu, B, i0) : B, of = -1, base = -1;
+    for (uint32_t i0 = per * gt; i0 < n_slots; i0 += per * step) {
+        int b = i0 < (uint32_t)added ? last_at_most(s_cu, B, (int)i0) : B, of = -1, base = -1;
 #pragma unroll 1
         for (int e = 0; e < per; ++e) {
-            const int i = i0 + e;
+            if (i0 + e >= n_slots) break;
+            const int i = (int)(i0 + e);
             int slot = -1;
             if (i < added) {
                 while (i >= s_cu[b + 1]) {
@@ -186,7 +188,7 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const iskv_page_pla
                 }
                 slot = base < 0 ? -1 : base + pos % kPage;
             }
-            if (i < a.tokens) a.slots[i] = slot;
+            a.slots[i] = slot;
         }
     }
     for (int j = gt; j < fresh; j += step) {

@@ -144,3 +144,23 @@ def test_the_largest_batch():
     free = np.concatenate([order[at:], np.zeros(at, dtype=np.int32)])
     *_, status = _step_both(lens, add, table, free, 9000, int(np.maximum(add, 0).sum()) + 3, in_place=True)
     assert status == 0
+
+
+@pytest.mark.parametrize("refused", [False, True])
+def test_as_many_slots_as_an_int32_counts(refused):
+    import online_rank_kv_b200 as ik
+    n = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 4 * n + (2 << 30):
+        pytest.skip("needs 8 GiB for the slots")
+    out = ik.PagePlan.empty(2, n)
+    out.slots.fill_(-77)
+    table, free = torch.full((2, 4), -1, dtype=torch.int32, device="cuda"), _dev(np.arange(8))
+    ik.page_plan(_dev([0, 0]), _dev([100, 257 if refused else 30]), table, free, _dev([8]), out=out)
+    torch.cuda.synchronize()
+    assert out.status.item() == (-4 if refused else 0)
+    assert out.cu.tolist() == ([0, 0, 0] if refused else [0, 100, 130])
+    first = 0 if refused else 130
+    want = [] if refused else [7 * 64 + i for i in range(64)] + [6 * 64 + i for i in range(36)] + [5 * 64 + i for i in range(30)]
+    assert out.slots[:first].tolist() == want
+    assert int(out.slots[first:].max()) == -1 and int(out.slots[first:].min()) == -1
+    assert free.tolist() == list(range(8))
