@@ -377,6 +377,20 @@ def _launch(device: int, fn, where: str, *args, stream=None) -> None:
         raise IskvError(code, where)
 
 
+def _new_on(stream, make):
+    """make()'s tensors for a call on `stream` (None: the current one).  They
+    come from that stream's pool, whose earlier work is done with the memory
+    when the call runs, and go back to it only when the current stream, where
+    the caller reads them, has passed them too."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        new = make()
+    for t in new:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return new
+
+
 def _int32(device: int, shape, t: torch.Tensor, name: str) -> int:
     if t.dtype is not torch.int32 or t.get_device() != device or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on cuda:{device}")
@@ -412,6 +426,9 @@ class PagePlan:
             return torch.empty(n, dtype=torch.int32, device=device)
         return cls(e(batch), e(batch + 1), e(tokens), e(1), e(1))
 
+    def _all(self):
+        return self.lens, self.cu, self.slots, self.n_free, self.status
+
 
 def page_plan(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, free: torch.Tensor,
               n_free: torch.Tensor, tokens: int | None = None, out: PagePlan | None = None,
@@ -430,7 +447,7 @@ def page_plan(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, free: 
     if out is None:
         if tokens is None:
             raise ValueError("tokens (the number of slots) or out is needed")
-        out = PagePlan.empty(batch, tokens, lens.device)
+        out = PagePlan(*_new_on(stream, lambda: PagePlan.empty(batch, tokens, lens.device)._all()))
     n, pages = out.slots.shape[0], free.shape[0]
     every = (lens, add, table, free, n_free, out.lens, out.cu, out.slots, out.n_free, out.status)
     sizes = (batch, batch, batch * width, pages, 1, batch, batch + 1, n, 1, 1)
@@ -528,7 +545,7 @@ class Q8Pages:
         if q.requires_grad and torch.is_grad_enabled():
             raise ValueError("attention over 8-bit pages is forward only: detach q")
         if out is None:
-            out = q.new_empty(q.shape)
+            out, = _new_on(stream, lambda: (q.new_empty(q.shape),))
         elif out.shape != q.shape or out.dtype != q.dtype or out.get_device() != dev or not out.is_contiguous():
             raise ValueError("out must be contiguous and match q in shape, type and device")
         if lens.dim() != 1 or table.dim() != 2:
@@ -543,7 +560,7 @@ class Q8Pages:
                 need = LIB.iskv_q8_workspace(heads, self.kv_heads, n, max_new, dt)
             if len(self._need) < 64:
                 self._need[(heads, max_new, dt)] = need
-        ws = q.new_empty(max(need, 0), dtype=torch.uint8)
+        ws, = _new_on(stream, lambda: (q.new_empty(max(need, 0), dtype=torch.uint8),))
         i32 = torch.int32
         if not (table.dtype is i32 and lens.dtype is i32 and cu.dtype is i32 and cu.numel() == batch + 1
                 and table.get_device() == dev and lens.get_device() == dev and cu.get_device() == dev
@@ -553,8 +570,7 @@ class Q8Pages:
                             out.data_ptr(), table.data_ptr(), lens.data_ptr(), cu.data_ptr(),
                             None if prefix is None else _int32(dev, (batch,), prefix, "prefix"),
                             None if slopes is None else slopes.data_ptr(), ws.data_ptr(), need, self._status_at)
-        if stream is not None:   # both come from the current stream's pool
-            ws.record_stream(stream)
+        if stream is not None:   # (an out of the caller's may be the current stream's)
             out.record_stream(stream)
         _launch(dev, LIB.iskv_q8_attention, "iskv_q8_attention", self._ref, ctypes.byref(args), stream=stream)
         return out

@@ -467,3 +467,35 @@ def test_no_queries_and_no_requests(max_new):
                           out=given)
     torch.cuda.synchronize()
     assert (out == 3.0).all() and store.status() == 0
+
+
+def test_calls_in_turn_on_two_streams_by_argument():
+    """Results and scratch memory of a call come from the stream it runs on:
+    calls on two streams in turn, none waiting for the other, give what they
+    give alone, and hold no memory of each other."""
+    import online_rank_kv_b200 as ik
+    cases = [Case([3000 + 700 * i, 90], [new, 1], 2, 4, ref.E4M3, seed=60 + i)
+             for i, new in enumerate([1, 150, 5])]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    args = []
+    for c in cases:
+        c.store()
+        cu = np.concatenate([[0], np.cumsum(c.new)])
+        args.append([torch.tensor(np.asarray(x), **i32) for x in (c.table, c.lens, cu)])
+    def call(i, stream):
+        table, lens, cu = args[i]
+        return cases[i].store().attention(cases[i].q, table, lens, cu, max_new=max(cases[i].new), stream=stream)
+    alone = [call(i, None) for i in range(3)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    outs = [(i, call(i, side if (k + i) % 2 else None)) for k in range(10) for i in range(3)]
+    lens, add = torch.zeros(3, **i32), torch.full((3,), 70, **i32)
+    table, free, n_free = torch.full((3, 2), -1, **i32), torch.arange(9, **i32), torch.full((1,), 9, **i32)
+    torch.cuda.synchronize()
+    plan = ik.page_plan(lens, add, table, free, n_free, tokens=211, stream=side)
+    junk = [torch.full((8192,), 7, **i32) for _ in range(8)]     # the current stream goes on
+    torch.cuda.synchronize()
+    for i, o in outs:
+        assert torch.equal(o, alone[i])
+    assert plan.cu.tolist() == [0, 70, 140, 210] and plan.n_free.item() == 3 and plan.status.item() == 0
+    assert all((j == 7).all() for j in junk)
