@@ -507,7 +507,7 @@ class Q8Pages:
     def _rows(self, t: torch.Tensor, heads: int | None, name: str) -> int:
         shape = t.shape
         if len(shape) != 3 or shape[2] != 128 or (heads is not None and shape[1] != heads) \
-                or (shape[0] > 0 and t.stride()[1:] != (128, 1)):
+                or (shape[0] > 0 and (t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != 128))):
             raise ValueError(f"{name} must be [tokens, heads, 128] with contiguous tokens")
         if t.get_device() != self._dev:
             raise ValueError(f"{name} must be on {self.device}")

@@ -201,3 +201,22 @@ def test_a_stream_of_its_own():
     b.append(x[0], x[1], slots, stream=s)
     s.synchronize()
     assert torch.equal(a.k, b.k) and torch.equal(a.v, b.v) and torch.equal(a.k_scale, b.k_scale)
+
+
+def test_one_head_of_a_transposed_tensor():
+    """The stride of a dimension of one element says nothing."""
+    import online_rank_kv_b200 as ik
+    x = torch.randn(1, 70, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(9))
+    x = x.transpose(0, 1)                       # [70, 1, 128], stride of the head: 70 * 128
+    assert x.stride() == (128, 70 * 128, 1)
+    slots = torch.arange(70, dtype=torch.int32, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    got = []
+    for t in (x, x.contiguous().view(70, 128).unsqueeze(1)):
+        pages = ik.Q8Pages(2, 1, ik.CODE_INT8)
+        pages.append(t, t, slots)
+        out = pages.attention(t, torch.tensor([[0, 1]], **i32), torch.tensor([70], **i32), torch.tensor([0, 70], **i32),
+                              max_new=70)
+        got.append((pages.k, pages.v_scale, out))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
