@@ -496,6 +496,8 @@ ISKV_API int iskv_q8_append(const iskv_q8_pages* store, const void* k, const voi
  * need one each.
  * *status is set to ISKV_ERR_DEVICE_TIMEOUT where a bounded wait inside the
  * kernel gave up (out is then incomplete) and is otherwise left.
+ * A query row is read by several blocks, so out may not overlap q's rows or the
+ * space between them (INVALID_ARG).
  * q_heads / kv_heads <= 8; ISKV_BF16 or ISKV_F32 queries; q, out and
  * workspace 16-byte aligned, q_stride a multiple of 16 bytes.
  * Errors: INVALID_ARG, UNSUPPORTED (head_dim, page, heads per group),

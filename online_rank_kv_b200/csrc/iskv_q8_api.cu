@@ -34,6 +34,11 @@ bool all_on_device(const void* const* ptrs, int n) {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
 int check_store(const iskv_q8_pages* s) {
     if (!s || s->pages < 1 || s->kv_heads < 1 || (int64_t)s->pages * ISKV_PAGE > INT32_MAX ||
         (int64_t)s->pages * s->kv_heads > INT32_MAX)
@@ -174,6 +179,8 @@ int iskv_q8_attention(const iskv_q8_pages* store, const iskv_q8_attention_args* 
     if (a->q_stride % (16 / elem_bytes(a->dtype)) != 0 ||
         (a->tokens > 1 && a->q_stride < (int64_t)a->q_heads * kHeadDim))
         return ISKV_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)a->q_heads * kHeadDim, es = elem_bytes(a->dtype);
+    if (overlap(a->q, ((a->tokens - 1) * a->q_stride + row) * es, a->out, a->tokens * row * es)) return ISKV_ERR_INVALID_ARG;
     const void* ptrs[] = {store->k, store->v, store->k_scale, store->v_scale, a->q, a->out, a->table, a->lens, a->cu,
                           a->prefix, a->slopes, a->workspace, a->status};
     if (!all_on_device(ptrs, 13)) return ISKV_ERR_INVALID_ARG;

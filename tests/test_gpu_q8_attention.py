@@ -499,3 +499,20 @@ def test_calls_in_turn_on_two_streams_by_argument():
         assert torch.equal(o, alone[i])
     assert plan.cu.tolist() == [0, 70, 140, 210] and plan.n_free.item() == 3 and plan.status.item() == 0
     assert all((j == 7).all() for j in junk)
+
+
+@pytest.mark.parametrize("new", [1, 150])
+def test_an_output_over_the_queries_is_refused(new):
+    import online_rank_kv_b200 as ik
+    c = Case([700, 333], [new, new], 2, 4, ref.INT8, seed=27)
+    n = c.q.shape[0]
+    both = torch.zeros(2 * n, c.heads, 128, dtype=c.dtype, device="cuda")
+    both[:n] = c.q
+    c.q = both[:n]
+    for at in (0, 1, n - 1):
+        with pytest.raises(ik.IskvError) as e:
+            c.run(out=both[at:at + n])
+        assert e.value.code == -1
+    got = c.run(out=both[n:]).double().cpu().numpy()      # right behind them
+    w, tol = c.want()
+    assert (np.abs(got - w) <= tol).all()
