@@ -992,7 +992,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
 // a time, its partials' maxima in the lanes.
 __global__ void __launch_bounds__(256) q8_prompt_join_kernel(const AttnArgs p) {
     const int cta = blockIdx.x, lane = threadIdx.x & 31;
-    let_next();
+    // (no let_next(): 558 us with it, 555 without for one prompt of 8192 tokens,
+    // 1285 against 1254 for 8 layers of 512 new ones behind up to 20K)
     after_previous();
     const int* m = p.meta + cta * kMeta;
     if (m[1] == 0) return;

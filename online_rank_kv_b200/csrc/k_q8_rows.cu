@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(256) q8_join_kernel(const __grid_constant__ At
     constexpr int R = 8 * NT, kWarps = Shape<NT, F32>::kWarps, kPartsPerCta = 2 * kWarps + 2;
     const int cta = blockIdx.x, row = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     __shared__ float s_ml[8][2], s_o[8][kHeadDim];
-    let_next();
+    // (no let_next(): eight layers of 64 requests 359 us without, 362 with it)
     after_previous();
     const int4 m = *reinterpret_cast<const int4*>(p.meta + cta * kMeta);
     if (m.y == 0) return;

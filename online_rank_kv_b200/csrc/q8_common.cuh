@@ -37,8 +37,9 @@ struct SmemOnce {
 
 // Launches a kernel that may come up while the one before it in the stream ends.
 // It calls after_previous() before it touches memory, which waits for that
-// kernel's end and its writes; kernels call let_next() at once, so that what
-// follows them need not wait for its own launch. A page plan and eight layers of
+// kernel's end and its writes; kernels but the joins call let_next() at once, so
+// that what follows them need not wait for its own launch. (A grid that is up
+// while a join's many blocks run slows them by more than its launch.) A page plan and eight layers of
 // append and attention, 1000 keys a request: batch 1 119 -> 113 us as a graph,
 // batch 64 394 -> 364 us launched one by one (387 -> 386 as a graph).
 template <typename... P, typename... A>
