@@ -42,6 +42,7 @@
 #include <cuda.h>
 
 #include "q8_common.cuh"
+#include "q8_split.h"
 #include "tc_util.cuh"
 
 namespace iskv {
@@ -362,12 +363,10 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
         at.b = s_b[warp];
         at.load(p);
         {
-            int64_t off = s_off[warp];
-            const int64_t per_head = (int64_t)at.tiles * at.r.steps;
-            at.h = (int)(off / per_head);
-            const int rest = (int)(off - at.h * per_head);
-            at.tile = rest / at.r.steps;
-            at.step = rest - at.tile * at.r.steps;
+            const StepPlace s = place_of_step(s_off[warp], at.tiles, at.r.steps);
+            at.h = s.h;
+            at.tile = s.tile;
+            at.step = s.step;
         }
         in = at;
         int left = (int)min(n_steps, (int64_t)INT32_MAX), to_issue = left;
