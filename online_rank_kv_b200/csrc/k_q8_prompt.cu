@@ -463,9 +463,12 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
             const float lsv = st.lsv, isv = st.isv;
             const int left = st.left;
             __syncwarp();
-            if (left != 0 && lane == 0) tc::mbar_arrive(&sh.info_empty[n % kSteps]);
+            // (a piece's first step is given back behind its scores: the MMA warp
+            // has read it then)
+            if (left != 0 && !first && lane == 0) tc::mbar_arrive(&sh.info_empty[n % kSteps]);
             ok = __all_sync(0xffffffffu, wait_for(sh, &sh.s_full[i][n & 1], (n >> 1) & 1));
             if (!ok) return;
+            if (left != 0 && first && lane == 0) tc::mbar_arrive(&sh.info_empty[n % kSteps]);
             tc::tc_fence_after();
             uint32_t s[kN];
             tmem_ld32(tSn, *reinterpret_cast<uint32_t(*)[32]>(s));
@@ -655,8 +658,9 @@ __device__ __forceinline__ bool elect() {
 }
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
-// Tile i's MMAs.  A step's description is read where a piece begins only: the
-// walk cannot overwrite it before, since this step's softmax has not run.
+// Tile i's MMAs.  A step's description is read where a piece begins only, without
+// an arrival of its own: the softmax warps of both tiles give a piece's first step
+// back behind its scores, which either MMA warp issues after this read.
 __device__ __forceinline__ void mma_role(Shared& sh, uint32_t aK, uint32_t aQ, uint32_t tmem, int i) {
     constexpr uint32_t idS = tc::idesc_f32acc(0, kM, kN, 0, 0), idO = tc::idesc_f32acc(0, kM, kHeadDim, 0, 1);
     const uint64_t dK = desc_sw128(aK, 16, 1024), dQ = desc_sw128(aQ + i * kQBytes, 16, 1024);

@@ -8,6 +8,7 @@ import torch
 
 from oracle import paged_q8 as ref
 from q8_testlib import bound
+from test_gpu_q8_attention import Case
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +38,17 @@ def test_a_head_with_more_than_two_to_the_31_steps():
         floor = 2.0 ** -37 * np.abs(vv[:i + 1]).sum(0)
         assert (np.abs(out[i].double().cpu().numpy() - o[0]) <= (bound(o, mass, size, torch.bfloat16) + floor)[0]).all(), i
     assert torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("kv_heads,mod", [(2, {}), (5, dict(cap=20.0)), (2, dict(window=40))])
+def test_many_short_prompts_in_a_row(kv_heads, mod):
+    """Some ten pieces of one to eleven pages per CTA: step descriptions are handed
+    round and round the prompt kernel's ring, first steps close behind last ones."""
+    rng = np.random.default_rng(32)
+    lens = rng.integers(40, 700, 420).tolist()
+    c = Case(lens, [int(rng.integers(33, 41)) for _ in lens], kv_heads, 4, ref.INT8, seed=33)
+    c.check(**mod)
+    a = c.run(**mod)
+    for _ in range(20):
+        assert torch.equal(a, c.run(**mod))
+    assert c.store().status() == 0
