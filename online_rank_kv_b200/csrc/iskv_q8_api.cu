@@ -2,6 +2,8 @@
 // the choice of kernel, launches.  Nothing is allocated or kept here.
 #include <nvtx3/nvToolsExt.h>
 
+#include <cstdlib>
+
 #include "q8_common.cuh"
 
 using namespace iskv;
@@ -61,6 +63,18 @@ int sm_count() {
         return 148;
     }
     return n;
+}
+
+// Clock cycles a pipeline wait of the attention kernels may take before the call
+// gives up with DEVICE_TIMEOUT; tests shorten it through the environment to make
+// waits run out on purpose (ISKV_TEST_PIPELINE_WAIT_CYCLES, read at the first call).
+long long wait_cycles() {
+    static const long long w = [] {
+        const char* e = std::getenv("ISKV_TEST_PIPELINE_WAIT_CYCLES");
+        const long long n = e ? std::atoll(e) : 0;
+        return n > 0 ? n : tc::kWaitCycles;
+    }();
+    return w;
 }
 
 // Row tiles of the split kernel in eights of rows.  Several tiles of a request
@@ -218,6 +232,8 @@ int iskv_q8_attention(const iskv_q8_pages* store, const iskv_q8_attention_args* 
     p.ml = p.part + parts * kHeadDim;
     p.meta = reinterpret_cast<int*>(p.ml + parts * 2);
     p.status = a->status;
+    p.wait_cycles = wait_cycles();
+    p.patient = p.wait_cycles >= tc::kWaitCycles;
     p.whole = whole_items(a->width, a->batch, store->kv_heads, p.ctas);
     if (prompt)
         return q8::launch_q8_prompt(p, store->code, s) == cudaSuccess ? ISKV_OK : ISKV_ERR_CUDA;

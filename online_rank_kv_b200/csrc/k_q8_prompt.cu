@@ -226,9 +226,9 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uin
 }
 
 // Waits are bounded: the limit is about a second, a pipeline step microseconds.
-__device__ __forceinline__ bool wait_longer(Shared& sh, uint64_t* bar, uint32_t parity) {
-    const long long deadline = clock64() + tc::kWaitCycles;
-    while (!tc::mbar_try_wait(bar, parity)) {
+__device__ __forceinline__ bool wait_longer(const AttnArgs& p, Shared& sh, uint64_t* bar, uint32_t parity) {
+    const long long deadline = clock64() + p.wait_cycles;
+    while (!try_phase(p, bar, parity)) {
         if (*(volatile int*)&sh.failed) return false;
         if (clock64() > deadline) {
             sh.failed = 1;
@@ -237,8 +237,13 @@ __device__ __forceinline__ bool wait_longer(Shared& sh, uint64_t* bar, uint32_t 
     }
     return true;
 }
-__device__ __forceinline__ bool wait_for(Shared& sh, uint64_t* bar, uint32_t parity) {
-    return tc::mbar_try_wait(bar, parity) || wait_longer(sh, bar, parity);
+// A lane's wait, and a warp's.  When one has given up, the warp's lanes leave their
+// role together: lanes apart would miss each other at the next warp or CTA barrier.
+__device__ __forceinline__ bool lane_wait(const AttnArgs& p, Shared& sh, uint64_t* bar, uint32_t parity) {
+    return tc::mbar_try_wait(bar, parity) || wait_longer(p, sh, bar, parity);
+}
+__device__ __forceinline__ bool wait_for(const AttnArgs& p, Shared& sh, uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, lane_wait(p, sh, bar, parity));
 }
 
 // The steps that a pair of query tiles sees.
@@ -356,7 +361,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
         }
     };
     {
-        const bool ok = __all_sync(0xffffffffu, wait_for(sh, &sh.info_full[0], 0));
+        const bool ok = wait_for(p, sh, &sh.info_full[0], 0);
         if (!ok || (sh.step[0].flags & kEnd)) return;
         load(sh.step[0]);
     }
@@ -451,7 +456,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
 
         for (bool first = true;; first = false) {   // steps
             const Step& st = sh.step[n % kSteps];
-            bool ok = __all_sync(0xffffffffu, wait_for(sh, &sh.info_full[n % kSteps], (n / kSteps) & 1));
+            bool ok = wait_for(p, sh, &sh.info_full[n % kSteps], (n / kSteps) & 1);
             if (!ok) return;
             const uint32_t tSn = tS + (n & 1) * kN;
             const int key0 = st.key0;
@@ -466,7 +471,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
             // (a piece's first step is given back behind its scores: the MMA warp
             // has read it then)
             if (left != 0 && !first && lane == 0) tc::mbar_arrive(&sh.info_empty[n % kSteps]);
-            ok = __all_sync(0xffffffffu, wait_for(sh, &sh.s_full[i][n & 1], (n >> 1) & 1));
+            ok = wait_for(p, sh, &sh.s_full[i][n & 1], (n >> 1) & 1);
             if (!ok) return;
             if (left != 0 && first && lane == 0) tc::mbar_arrive(&sh.info_empty[n % kSteps]);
             tc::tc_fence_after();
@@ -513,7 +518,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
                 huge = __any_sync(0xffffffffu, M > -INFINITY && fabsf(M) >= 1024.f);
                 l *= f;
                 if (!first) {   // the accumulator holds earlier steps
-                    ok = __all_sync(0xffffffffu, wait_for(sh, &sh.pv_done[i][(n - 1) & 1], ((n - 1) >> 1) & 1));
+                    ok = wait_for(p, sh, &sh.pv_done[i][(n - 1) & 1], ((n - 1) >> 1) & 1);
                     if (!ok) return;
                     tc::tc_fence_after();
 #pragma unroll 1
@@ -582,11 +587,11 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
             if (lane == 0) tc::mbar_arrive(&sh.info_empty[n % kSteps]);
         }
         const int last = n++;
-        bool ok = __all_sync(0xffffffffu, wait_for(sh, &sh.info_full[n % kSteps], (n / kSteps) & 1));
+        bool ok = wait_for(p, sh, &sh.info_full[n % kSteps], (n / kSteps) & 1);
         if (!ok) return;
         more = !(sh.step[n % kSteps].flags & kEnd);
         if (more) load(sh.step[n % kSteps]);
-        ok = __all_sync(0xffffffffu, wait_for(sh, &sh.pv_done[i][last & 1], (last >> 1) & 1));
+        ok = wait_for(p, sh, &sh.pv_done[i][last & 1], (last >> 1) & 1);
         if (!ok) return;
         tc::tc_fence_after();
     }
@@ -623,22 +628,21 @@ __device__ __forceinline__ void code_tile(uint8_t* tile, const uint8_t* codes, i
 }
 
 template <int CODE>
-__device__ __forceinline__ void code_role(Shared& sh, uint8_t* sK, const uint8_t* sKc, int u, int lane) {
+__device__ __forceinline__ void code_role(const AttnArgs& p, Shared& sh, uint8_t* sK, const uint8_t* sKc, int u, int lane) {
     for (int n = 0;; ++n) {
         const Step& st = sh.step[n % kSteps];
-        if (!wait_for(sh, &sh.info_full[n % kSteps], (n / kSteps) & 1) || (st.flags & kEnd)) return;
+        bool ok = lane_wait(p, sh, &sh.info_full[n % kSteps], (n / kSteps) & 1);
         const int rows = st.page >= 0 ? st.len - st.key0 : 0;
-        __syncwarp();
+        if (!__all_sync(0xffffffffu, ok && !(st.flags & kEnd))) return;
         if (lane == 0) tc::mbar_arrive(&sh.info_empty[n % kSteps]);
         const int bf = n % kBuffers;
 #pragma unroll 1
         for (int v = 0; v < 2; ++v) {   // K, then V
-            if (!wait_for(sh, &sh.c_full[v][n & 1], (n >> 1) & 1) ||
-                !wait_for(sh, &sh.empty[v][bf], ((n / kBuffers) & 1) ^ 1))
-                return;
-            code_tile<CODE>(sK + (kBuffers * v + bf) * kTileBytes, sKc + (2 * v + (n & 1)) * kCodeBytes, u, rows);
+            ok = lane_wait(p, sh, &sh.c_full[v][n & 1], (n >> 1) & 1) &&
+                 lane_wait(p, sh, &sh.empty[v][bf], ((n / kBuffers) & 1) ^ 1);
+            if (ok) code_tile<CODE>(sK + (kBuffers * v + bf) * kTileBytes, sKc + (2 * v + (n & 1)) * kCodeBytes, u, rows);
             tc::fence_async_smem();
-            __syncwarp();
+            if (!__all_sync(0xffffffffu, ok)) return;
             if (lane == 0) {
                 tc::mbar_arrive(&sh.full[v][bf]);
                 tc::mbar_arrive(&sh.c_empty[v][n & 1]);
@@ -661,13 +665,13 @@ __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, 
 // Tile i's MMAs.  A step's description is read where a piece begins only, without
 // an arrival of its own: the softmax warps of both tiles give a piece's first step
 // back behind its scores, which either MMA warp issues after this read.
-__device__ __forceinline__ void mma_role(Shared& sh, uint32_t aK, uint32_t aQ, uint32_t tmem, int i) {
+__device__ __forceinline__ void mma_role(const AttnArgs& p, Shared& sh, uint32_t aK, uint32_t aQ, uint32_t tmem, int i) {
     constexpr uint32_t idS = tc::idesc_f32acc(0, kM, kN, 0, 0), idO = tc::idesc_f32acc(0, kM, kHeadDim, 0, 1);
     const uint64_t dK = desc_sw128(aK, 16, 1024), dQ = desc_sw128(aQ + i * kQBytes, 16, 1024);
     const uint64_t dV = desc_sw128(aK + kBuffers * kTileBytes, kHalf, 1024);
     const uint32_t tS = tmem + 2 * i * kN, tO = tmem + 4 * kN + i * kHeadDim;
     const bool leader = elect();   // one lane for all: a commit covers its own thread's MMAs
-    auto waited = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_for(sh, bar, parity)); };
+    auto waited = [&](uint64_t* bar, uint32_t parity) { return wait_for(p, sh, bar, parity); };
     // scores of step n (descriptors step in units of 16 bytes); false: a wait gave up
     auto scores = [&](int n) {
         const int bf = n % kBuffers;
@@ -768,7 +772,7 @@ __device__ __forceinline__ void walk_role(const AttnArgs& p, Shared& sh, int sta
                 lsv = lg2(sv);
                 isv = __fdividef(1.f, sv);
             }
-            ok = __all_sync(0xffffffffu, wait_for(sh, &sh.info_empty[n % kSteps], ((n / kSteps) & 1) ^ 1));
+            ok = wait_for(p, sh, &sh.info_empty[n % kSteps], ((n / kSteps) & 1) ^ 1);
             if (!ok) break;
             if (lane == in) {
                 Step& st = sh.step[n % kSteps];
@@ -793,7 +797,7 @@ __device__ __forceinline__ void walk_role(const AttnArgs& p, Shared& sh, int sta
         if (ok) more = w.next(p);
     }
     if (ok) {
-        ok = __all_sync(0xffffffffu, wait_for(sh, &sh.info_empty[n % kSteps], ((n / kSteps) & 1) ^ 1));
+        ok = wait_for(p, sh, &sh.info_empty[n % kSteps], ((n / kSteps) & 1) ^ 1);
         if (ok && lane == 0) {
             sh.step[n % kSteps].flags = kEnd;
             tc::mbar_arrive(&sh.info_full[n % kSteps]);
@@ -805,7 +809,7 @@ __device__ __forceinline__ void walk_role(const AttnArgs& p, Shared& sh, int sta
 __device__ __forceinline__ void copy_role(const AttnArgs& p, Shared& sh, uint8_t* sKc, int lane) {
     bool ok = true;
     for (int n = 0;; ++n) {
-        ok = __all_sync(0xffffffffu, wait_for(sh, &sh.info_full[n % kSteps], (n / kSteps) & 1));
+        ok = wait_for(p, sh, &sh.info_full[n % kSteps], (n / kSteps) & 1);
         if (!ok || (sh.step[n % kSteps].flags & kEnd)) break;
         const int page = sh.step[n % kSteps].page;
         const int64_t at = ((int64_t)max(page, 0) * p.kv_heads + sh.step[n % kSteps].h) * kCodeBytes;
@@ -813,7 +817,7 @@ __device__ __forceinline__ void copy_role(const AttnArgs& p, Shared& sh, uint8_t
         if (lane == 0) tc::mbar_arrive(&sh.info_empty[n % kSteps]);
 #pragma unroll 1
         for (int v = 0; v < 2 && ok; ++v) {   // K, then V
-            ok = __all_sync(0xffffffffu, wait_for(sh, &sh.c_empty[v][n & 1], ((n >> 1) & 1) ^ 1));
+            ok = wait_for(p, sh, &sh.c_empty[v][n & 1], ((n >> 1) & 1) ^ 1);
             if (ok && lane == 0) {
                 uint64_t* bar = &sh.c_full[v][n & 1];
                 tc::mbar_arrive_expect_tx(bar, page >= 0 ? kCodeBytes : 0);
@@ -822,12 +826,6 @@ __device__ __forceinline__ void copy_role(const AttnArgs& p, Shared& sh, uint8_t
             __syncwarp();
         }
         if (!ok) break;
-    }
-    if (!ok) {
-        // copies may be on their way to readers that have given up: they land
-        // within microseconds; the CTA ends long after
-        const long long until = clock64() + 20000000;
-        while (clock64() < until) __nanosleep(1000);
     }
 }
 
@@ -972,11 +970,11 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
         softmax_role<MOD>(p, sh, sQ, tmem, warp, lane);
     } else if (warp < kSoftmaxWarps + kCodeWarps) {
         fewer_registers<kCodeRegs>();
-        code_role<CODE>(sh, sK, sKc, t - 32 * kSoftmaxWarps, lane);
+        code_role<CODE>(p, sh, sK, sKc, t - 32 * kSoftmaxWarps, lane);
     } else {
         fewer_registers<kOtherRegs>();
         if (warp == kMmaWarp || warp == kMmaWarp + 2) {
-            mma_role(sh, uniform(tc::smem_u32(sK)), uniform(tc::smem_u32(sQ)), uniform(tmem), uniform(warp - kMmaWarp) >> 1);
+            mma_role(p, sh, uniform(tc::smem_u32(sK)), uniform(tc::smem_u32(sQ)), uniform(tmem), uniform(warp - kMmaWarp) >> 1);
         } else if (warp == kWalkWarp) {
             walk_role(p, sh, start_h, left, lane);
         } else if (warp == kCopyWarp) {
@@ -987,8 +985,15 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prompt_kernel(const AttnArgs p
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
+    if (sh.failed) {
+        // copies may be on their way to readers that have given up: they land
+        // within microseconds; the CTA ends long after
+        if (t == 0 && p.status) atomicMin(p.status, ISKV_ERR_DEVICE_TIMEOUT);
+        const long long until = clock64() + 20000000;
+        while (clock64() < until) __nanosleep(1000);
+        __syncthreads();
+    }
     if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
-    if (t == 0 && sh.failed && p.status) atomicMin(p.status, ISKV_ERR_DEVICE_TIMEOUT);
 }
 
 // Pairs that several CTAs share: CTA c's partial 1 begins one, the partials 0

@@ -482,9 +482,10 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
             }
 
             __syncwarp();
-            if (!tc::mbar_try_wait(&s_full[warp][stage], (phase >> stage) & 1) &&
-                !tc::mbar_wait(&s_full[warp][stage], (phase >> stage) & 1, clock64() + tc::kWaitCycles))
-                failed = true;
+            if (!p.patient || !tc::mbar_try_wait(&s_full[warp][stage], (phase >> stage) & 1)) {
+                const long long deadline = clock64() + p.wait_cycles;
+                while (!failed && !try_phase(p, &s_full[warp][stage], (phase >> stage) & 1)) failed = clock64() > deadline;
+            }
             if (__any_sync(0xffffffffu, failed)) {   // out is left incomplete
                 failed = true;
                 gave_up = 1;

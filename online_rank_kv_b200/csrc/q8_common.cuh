@@ -5,6 +5,7 @@
 #include <atomic>
 
 #include "iskv_internal.cuh"
+#include "tc_util.cuh"
 
 namespace iskv {
 namespace q8 {
@@ -98,7 +99,23 @@ struct AttnArgs {
     float* ml;                 // their running maxima and sums
     int* status;               // sticky, or nullptr
     int* meta;                 // per CTA: what it leaves to be joined
+    long long wait_cycles;     // clock cycles that a wait may take
+    int patient;               // whether a try of a long wait may sleep (0: waits that must run out do)
 };
+
+// One try of a wait for the phase of a barrier.
+__device__ __forceinline__ bool try_phase(const AttnArgs& p, uint64_t* bar, uint32_t parity) {
+    if (p.patient) return tc::mbar_try_wait(bar, parity);
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 
 // ---------------------------------------------------------------------------
 // Codes to fp16, two at a time, exactly.

@@ -2,12 +2,16 @@
 lists past 2^31 steps, blocks of zeros, caps of any size, NaN, short lives of
 inputs, waits that run out."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
 
 from oracle import paged_q8 as ref
-from q8_testlib import bound
+from q8_testlib import bound, rows_of, step_floor
 from test_gpu_q8_attention import Case
 
 pytestmark = pytest.mark.gpu
@@ -52,3 +56,50 @@ def test_many_short_prompts_in_a_row(kv_heads, mod):
     for _ in range(20):
         assert torch.equal(a, c.run(**mod))
     assert c.store().status() == 0
+
+
+WAITS = r"""
+import sys
+sys.path[:0] = [sys.argv[1], sys.argv[1] + "/tests"]
+import torch
+import online_rank_kv_b200 as ik
+from test_gpu_q8_attention import Case
+from oracle import paged_q8 as ref
+for code in (ref.INT8, ref.E4M3):
+    for lens, dtype, new, mod in (([3000, 900, 160], "bf16", 1, {}), ([3000, 900, 160], "f32", 6, {}),
+                                  ([3000, 900, 160], "f32", 40, dict(cap=20.0)),
+                                  ([3000, 900, 160], "bf16", 150, {}),
+                                  ([3000, 900, 160], "bf16", 150, dict(window=200, cap=20.0)),
+                                  ([60000, 40000, 9000], "bf16", 1, {}), ([60000, 40000, 9000], "f32", 40, dict(cap=20.0)),
+                                  ([60000, 40000, 9000], "bf16", 150, {})):
+        c = Case(lens, [new] * 3, 2, 4, code, dtype, seed=34)
+        for _ in range(2):
+            out = c.run(**mod)
+            torch.cuda.synchronize()
+            print("call", sum(lens), dtype, new, c.store().status(), flush=True)
+x = torch.ones(256, 256, device="cuda")
+assert ((x @ x) == 256).all()
+store = ik.Q8Pages(2, 2)
+i32 = dict(dtype=torch.int32, device="cuda")
+store.append(torch.ones(3, 2, 128, device="cuda"), torch.ones(3, 2, 128, device="cuda"), torch.arange(3, **i32))
+assert store.status() == 0 and (store.k[0, :, :3] == 127).all()
+print("alive")
+"""
+
+
+def test_waits_that_run_out_are_reported_and_leave_the_context_usable():
+    """A process whose pipeline waits may take one cycle (the waits that let
+    copies and products in flight end keep their limit): calls report the
+    timeout, none hangs, and the device goes on.  (A step of fp32
+    queries takes longer than the copies of the two steps behind it, and short
+    requests have few waits: theirs may not run out.)"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    env = dict(os.environ, ISKV_TEST_PIPELINE_WAIT_CYCLES="1")
+    out = subprocess.run([sys.executable, "-c", WAITS, root], env=env, capture_output=True, text=True, timeout=240)
+    assert out.returncode == 0, out.stderr[-2000:]
+    lines = out.stdout.split("\n")
+    calls = [line.split() for line in lines if line.startswith("call")]
+    assert len(calls) == 32 and all(c[-1] in ("0", "-8") for c in calls), out.stdout
+    for size, dtype, new, status in [c[1:] for c in calls]:
+        assert status == "-8" or dtype == "f32" or int(size) < 10000, out.stdout
+    assert "alive" in lines
