@@ -432,10 +432,14 @@ ISKV_API int iskv_page_plan(const iskv_page_plan_args* args, void* stream);
  *     2^e with the block's largest |x| <= 448 * 2^e, code = x / 2^e rounded
  *     half to even.
  * A block whose largest value is below 2^-64 is stored as zeros, scale 0.
- * Scales are 0 or in [2^-72, 2^122], and the value scales of the pages that one
- * query sees lie within a factor of 2^100 of each other (attention takes a key's
- * weight and its value scale in one fp32 number: pages further below the largest
- * may count as nothing); e4m3 codes are not NaN (iskv_q8_append
+ * Scales are 0 or in [2^-72, 2^122]; the rows of a page of scale 0 are zeros,
+ * whatever their codes.  The other value scales of the pages that one query sees
+ * lie within a factor of 2^100 of each other: attention takes a key's weight and
+ * its value scale in one number, so pages further below the largest may count as
+ * nothing.  In the weighted sum of V that number has fp16's range below the
+ * row's largest one: an output element may be off by 2^-25 (more than 32 query
+ * rows per KV head) or 2^-39 of the sum of its keys' |codes| times the largest
+ * value scale, beside its rounding.  e4m3 codes are not NaN (iskv_q8_append
  * writes nothing else).                                                     */
 #define ISKV_CODE_INT8 0
 #define ISKV_CODE_E4M3 1

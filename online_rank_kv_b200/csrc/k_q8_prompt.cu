@@ -7,7 +7,7 @@
 // only when a row's maximum has grown past it by more than 2^15, where weights
 // would leave fp16, so the accumulator in tensor memory is rescaled once or
 // twice per row, not per page.  (The largest weight is at least 1; at fp16's
-// smallest steps the others are off by 2^-25 of it.)
+// smallest steps the others are off by 2^-25 of it.)  Pages of scale 0 as there.
 //
 // One CTA per SM holds two tiles of 128 query rows (query tokens x the heads
 // that share a KV head) and goes through the keys in steps of one page:
@@ -81,7 +81,7 @@ struct Step {
     int flags, key0;
     int left;               // steps of the piece that follow
     int page;               // -1: there is none
-    float sk, lsv, isv;     // key scale, log2 of the value scale, its inverse
+    float sk, lsv, isv;     // key scale, log2 of the value scale, its inverse (0: a page of scale 0)
     int len, pre, n, first; // the request: tokens, prefix, queries, first query row
     int token0, h;          // the pair's first query, KV head
     int slot;               // partial slot, -1: the piece is the whole pair
@@ -453,6 +453,10 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
         M = -INFINITY;
         l = 0.f;
         bool huge = false;   // some row of the warp has |M| >= 2^10
+        // log2 of the scale that pages of scale 0 take: that of the first other page
+        // which the row sees (infinity: none yet, they count in scale 1)
+        float lz = INFINITY;
+        bool settled = false;
 
         for (bool first = true;; first = false) {   // steps
             const Step& st = sh.step[n % kSteps];
@@ -465,8 +469,9 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
                                ((key0 + kN - 1 <= wp_min && (p.window == 0 || key0 > wp_max - p.window)) || key0 + kN <= pre);
             // the smallest normal number in place of zero keeps hidden scores at -inf
             float a = fmaxf(rowf * st.sk, 1.17549435e-38f);
-            const float lsv = st.lsv, isv = st.isv;
+            float lsv = st.lsv, isv = st.isv;
             const int left = st.left;
+            const bool valued = isv > 0.f;
             __syncwarp();
             // (a piece's first step is given back behind its scores: the MMA warp
             // has read it then)
@@ -509,6 +514,20 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
                 for (int e = 0; e < kN; e += 2)
                     m[(e >> 1) & 3] = max3(m[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
                 top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+            }
+            if (!(valued && settled)) {
+                if (!valued) {
+                    lsv = lz < INFINITY ? lz : 0.f;
+                    isv = ex2(-lsv);
+                } else {
+                    if (top > -INFINITY && lz == INFINITY) {   // what came before counted in scale 1
+                        M += lsv;
+                        l *= isv;
+                        lz = lsv;
+                    }
+                    settled = __all_sync(0xffffffffu, lz < INFINITY);
+                    huge = __any_sync(0xffffffffu, M > -INFINITY && fabsf(M) >= 1024.f);
+                }
             }
             const float now = fmaf(top, a, lsv);
             const bool raise = now > M + kRaise || (M == -INFINITY && now > -INFINITY);
@@ -633,6 +652,7 @@ __device__ __forceinline__ void code_role(const AttnArgs& p, Shared& sh, uint8_t
         const Step& st = sh.step[n % kSteps];
         bool ok = lane_wait(p, sh, &sh.info_full[n % kSteps], (n / kSteps) & 1);
         const int rows = st.page >= 0 ? st.len - st.key0 : 0;
+        const bool valued = st.isv > 0.f;   // (what scale 0 multiplies is nothing, whatever the codes)
         if (!__all_sync(0xffffffffu, ok && !(st.flags & kEnd))) return;
         if (lane == 0) tc::mbar_arrive(&sh.info_empty[n % kSteps]);
         const int bf = n % kBuffers;
@@ -640,7 +660,7 @@ __device__ __forceinline__ void code_role(const AttnArgs& p, Shared& sh, uint8_t
         for (int v = 0; v < 2; ++v) {   // K, then V
             ok = lane_wait(p, sh, &sh.c_full[v][n & 1], (n >> 1) & 1) &&
                  lane_wait(p, sh, &sh.empty[v][bf], ((n / kBuffers) & 1) ^ 1);
-            if (ok) code_tile<CODE>(sK + (kBuffers * v + bf) * kTileBytes, sKc + (2 * v + (n & 1)) * kCodeBytes, u, rows);
+            if (ok) code_tile<CODE>(sK + (kBuffers * v + bf) * kTileBytes, sKc + (2 * v + (n & 1)) * kCodeBytes, u, v == 0 || valued ? rows : 0);
             tc::fence_async_smem();
             if (!__all_sync(0xffffffffu, ok)) return;
             if (lane == 0) {
@@ -767,10 +787,9 @@ __device__ __forceinline__ void walk_role(const AttnArgs& p, Shared& sh, int sta
                 if (page >= p.pages) page = -1;
                 const int64_t at = (int64_t)max(page, 0) * p.kv_heads + w.h;
                 sk = page >= 0 ? __ldg(p.k_scale + at) : 0.f;
-                float sv = page >= 0 ? __ldg(p.v_scale + at) : 1.f;
-                if (!(sv > 0.f)) sv = 1.f;   // a block of zeros
+                const float sv = page >= 0 ? __ldg(p.v_scale + at) : 0.f;
                 lsv = lg2(sv);
-                isv = __fdividef(1.f, sv);
+                isv = sv > 0.f ? __fdividef(1.f, sv) : 0.f;
             }
             ok = wait_for(p, sh, &sh.info_empty[n % kSteps], ((n / kSteps) & 1) ^ 1);
             if (!ok) break;

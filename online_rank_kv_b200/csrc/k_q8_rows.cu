@@ -7,7 +7,11 @@
 // One exponential carries the value scale too: with
 //     w = 2^(score log2 e + log2 s_v - M),  M the running maximum,
 // the numerator is sum w c_v and the denominator sum w / s_v, whose factor
-// 1 / s_v is one number per page.  Codes are exact in fp16.  Queries are
+// 1 / s_v is one number per page.  (A page of scale 0 counts in the denominator
+// alone.  It takes the scale of the first other page that the row sees; a row that
+// has seen none counts in scale 1 and changes over then.  So its weights neither
+// raise M above those of small values, whose fp16 weights would lose bits, nor
+// vanish beside large ones.)  Codes are exact in fp16.  Queries are
 // multiplied by a power of two per row (their largest element then lies in
 // [2^14, 2^15)) and are exact in fp16 down to 2^-38 of it for bf16 input; fp32
 // queries, and the weights that go with them, take two fp16 parts (22 bits).
@@ -376,8 +380,9 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
         int pos[NT][2], see_from[NT][2];       // the causal span (see_from, pos]
         float slope[NT][2];
         float M[NT][2], l[NT][2], o[NT][8][4];
+        float lz[NT][2];                       // log2 of the scale for pages of scale 0; infinity: none yet
         int pmin = 0, pmax = 0, first_step = 0;
-        bool fresh = true;
+        bool fresh = true, settled = false;    // settled: every row has its lz
 
         auto page_of = [&](const Cursor& c) {
             const int tok = c.r.step_of(c.step) * kStepTokens;
@@ -413,6 +418,7 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
 
             if (fresh) {   // an item begins: its queries
                 fresh = false;
+                settled = false;
                 first_step = at.step;
                 pmin = at.r.len - at.r.n + at.tile * p.tq;
                 pmax = min(at.r.len - 1, pmin + p.tq - 1);
@@ -473,6 +479,7 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
                         see_from[n][c] = p.window > 0 ? max(-1, pos[n][c] - p.window) : -1;
                         M[n][c] = -INFINITY;
                         l[n][c] = 0.f;
+                        lz[n][c] = INFINITY;
                     }
 #pragma unroll
                     for (int m = 0; m < 8; ++m)
@@ -508,8 +515,7 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
             }
             const int64_t block = (int64_t)max(this_page, 0) * p.kv_heads + at.h;
             const float sk = __ldg(p.k_scale + block);
-            float sv = __ldg(p.v_scale + block);
-            sv = sv > 0.f ? sv : 1.f;                             // a block of zeros
+            const float sv = __ldg(p.v_scale + block);
             const uint32_t kb = ring_at + stage * kStageBytes, vb = kb + kStoreBytes;
             stage = stage + 1 == kStages ? 0 : stage + 1;
 
@@ -544,14 +550,16 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
             }
 
             // ---- weights ---------------------------------------------------
-            const float lsv = lg2(sv), isv = __fdividef(1.f, sv);
+            const bool valued = sv > 0.f;
+            const float lsv = valued ? lg2(sv) : 0.f, isv = __fdividef(1.f, sv);
             const bool whole = tok + kStepTokens <= stop &&
                                ((tok + kStepTokens - 1 <= pmin && (p.window == 0 || tok > pmax - p.window)) ||
                                 tok + kStepTokens <= at.r.pre);
             uint32_t pf[PARTS][NT][2][2];   // P^T as B fragments: [16-token half][8 tokens]
+            bool unsettled = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                float top[2] = {-INFINITY, -INFINITY};
+                float top[2] = {-INFINITY, -INFINITY}, is[2] = {isv, isv};
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -576,6 +584,26 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
                     top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], 4));
                     top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], 8));
                     top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], 16));
+                }
+                if (!(valued && settled)) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        if (!valued) {
+                            const float ls = lz[n][c] < INFINITY ? lz[n][c] : 0.f;
+                            is[c] = ex2(-ls);
+                            top[c] += ls;
+#pragma unroll
+                            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                                for (int e = c; e < 4; e += 2) sc[n][m][e] += ls;
+                        } else if (top[c] > -INFINITY && lz[n][c] == INFINITY) {   // what came before counted in scale 1
+                            M[n][c] += lsv;
+                            l[n][c] *= isv;
+                            lz[n][c] = lsv;
+                        }
+                    }
+                    unsettled |= fmaxf(lz[n][0], lz[n][1]) == INFINITY;
+                    if (n == NT - 1) settled = settled || __all_sync(0xffffffffu, !unsettled);
                 }
                 const bool grew = top[0] > M[n][0] || top[1] > M[n][1];
                 if (__any_sync(0xffffffffu, grew)) {
@@ -603,7 +631,7 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
                             sc[n][m][e] = ex2(sc[n][m][e] - base);
                             sum[c] += sc[n][m][e];
                         }
-                    l[n][c] += sum[c] * isv;
+                    l[n][c] += sum[c] * is[c];
                 }
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
@@ -611,10 +639,10 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
                     for (int i2 = 0; i2 < 2; ++i2) {
                         const float a = sc[n][m][2 * i2], b = sc[n][m][2 * i2 + 1];
                         const uint32_t hi = pack(a, b);
-                        pf[0][n][m][i2] = transpose8(hi);
+                        pf[0][n][m][i2] = transpose8(valued ? hi : 0u);   // (what scale 0 multiplies is nothing, whatever the codes)
                         if (F32) {
                             const float2 f = unpack(hi);
-                            pf[PARTS - 1][n][m][i2] = transpose8(pack(a - f.x, b - f.y));
+                            pf[PARTS - 1][n][m][i2] = transpose8(valued ? pack(a - f.x, b - f.y) : 0u);
                         }
                     }
             }

@@ -103,3 +103,45 @@ def test_waits_that_run_out_are_reported_and_leave_the_context_usable():
     for size, dtype, new, status in [c[1:] for c in calls]:
         assert status == "-8" or dtype == "f32" or int(size) < 10000, out.stdout
     assert "alive" in lines
+
+
+ZERO_PAGES = [[0], [1], [0, 1], [5], [0, 2, 4, 6, 8, 10, 12, 14], [15], list(range(1, 15)), list(range(16))]
+
+
+@pytest.mark.parametrize("code", [ref.INT8, ref.E4M3])
+@pytest.mark.parametrize("zeros", range(len(ZERO_PAGES)))
+@pytest.mark.parametrize("spread", [2.0 ** -20, 2.0 ** -40, 2.0 ** 40])
+@pytest.mark.parametrize("dtype,new", [("bf16", 1), ("f32", 3), ("bf16", 150)])
+def test_pages_without_values_beside_small_ones(code, zeros, spread, dtype, new):
+    """Pages of scale 0 count in the denominator and in nothing else: they do not
+    take bits from pages whose values are small (or weigh nothing beside large
+    ones).  Half of them hold codes: what scale 0 multiplies is zero."""
+    c = Case([1000, 300], [new, new], 2, 4, code, dtype, seed=37, spread=spread)
+    for b, width in ((0, 16), (1, 5)):
+        for j in ZERO_PAGES[zeros]:
+            if j < width:
+                p = c.table[b, j]
+                c.vs[p] = 0
+                if j % 2 == 0:
+                    c.vc[p] = 0
+    c.check()
+
+
+@pytest.mark.parametrize("lead", [31, 32, 33, 70])
+@pytest.mark.parametrize("new", [1, 200])
+def test_many_pages_without_values_in_front(lead, new):
+    c = Case([80 * 64], [new], 1, 8, ref.INT8, seed=38, spread=2.0 ** -30)
+    c.vs[c.table[0, :lead]] = 0
+    c.vc[c.table[0, :lead]] = 0
+    c.check()
+
+
+@pytest.mark.parametrize("new", [1, 200])
+def test_hidden_pages_do_not_weigh_pages_without_values(new):
+    """A sliding window over pages without values and pages 98 powers of two
+    apart, which no query sees together."""
+    c = Case([900], [new], 2, 4, ref.INT8, seed=39)
+    c.vs[:] = np.float32(2.0 ** 60)
+    c.vs[c.table[0, ::3]] = np.float32(2.0 ** -38)
+    c.vs[c.table[0, 1::3]] = 0
+    c.check(window=30)
