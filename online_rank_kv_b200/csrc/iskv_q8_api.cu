@@ -2,6 +2,8 @@
 // the choice of kernel, launches.  Nothing is allocated or kept here.
 #include <nvtx3/nvToolsExt.h>
 
+#include <cfloat>
+#include <cmath>
 #include <cstdlib>
 
 #include "q8_common.cuh"
@@ -222,6 +224,7 @@ int iskv_q8_attention(const iskv_q8_pages* store, const iskv_q8_attention_args* 
     p.window = a->window;
     p.scale = a->scale;
     p.cap = a->cap;
+    p.cap_inv = a->cap > 0.f ? std::fmin(1.f / a->cap, FLT_MAX) : 0.f;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int tiles8 = row_tiles8(g, a->max_new, a->dtype);
     const bool prompt = is_prompt(g, a->max_new, a->dtype);

@@ -490,7 +490,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
 #pragma unroll
                 for (int e = 0; e < kN; ++e) {
                     float y = __uint_as_float(s[e]) * a;
-                    if (p.cap > 0.f) y = p.cap * tanh_abs(__fdividef(y, p.cap));
+                    if (p.cap > 0.f) y = capped(y, p.cap, p.cap_inv);
                     s[e] = __float_as_uint(y * kLog2e - slope * fabsf(d0 - (float)e));
                 }
                 a = 1.f;

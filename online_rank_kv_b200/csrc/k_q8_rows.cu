@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
                         const int c = e & 1, key = tok + 16 * m + r + 8 * (e >> 1);
                         float x = sc[n][m][e] * (rowf[n][c] * sk);
                         if (MOD) {
-                            if (p.cap > 0.f) x = p.cap * tanh_abs(__fdividef(x, p.cap));
+                            if (p.cap > 0.f) x = capped(x, p.cap, p.cap_inv);
                             x *= kLog2e;
                             x -= slope[n][c] * fabsf((float)(pos[n][c] - key));
                         }

@@ -91,7 +91,7 @@ struct AttnArgs {
     int64_t tokens, q_stride;
     int batch, width, pages, kv_heads, g;
     int window;
-    float scale, cap;
+    float scale, cap, cap_inv;
     int tq;                    // query tokens per row tile
     int ctas;                  // CTAs
     int whole;                 // split kernel: a CTA takes whole items, none is joined across CTAs
@@ -164,10 +164,20 @@ __device__ __forceinline__ float lg2(float x) {
     return r;
 }
 
-// tanh(x) = 1 - 2 / (1 + e^(2x)): absolute error a few 2^-23 for every x, and
-// exact limits at both ends (e^(2x) reaches 0 and infinity).
-__device__ __forceinline__ float tanh_abs(float x) {
-    return 1.f - __fdividef(2.f, 1.f + ex2(2.f * kLog2e * x));
+// cap * tanh(x / cap), off by at most 2^-20 of x; inv: 1 / cap (host: finite).
+// Below half the cap it is x times a polynomial in (x / cap)^2 (minimax of the
+// relative error, 2^-26; 2^-23 with its roundings), which is exact for caps far
+// above x; from there on cap (1 - 2 / (1 + e^(2t))), whose error of a few 2^-23 of
+// the cap is one of 2^-21 of tanh there, and whose limits are exact (e^(2t)
+// reaches 0 and infinity).
+__device__ __forceinline__ float capped(float x, float cap, float inv) {
+    const float t = x * inv, u = t * t;
+    float y = fmaf(0.01724136434495449f, u, -0.05304544046521187f);
+    y = fmaf(y, u, 0.13325878977775574f);
+    y = fmaf(y, u, -0.333331435918808f);
+    y = x * fmaf(y, u, 1.f);
+    if (!(fabsf(t) < 0.5f)) y = cap * (1.f - __fdividef(2.f, 1.f + ex2(2.f * kLog2e * t)));
+    return y;
 }
 
 // ---------------------------------------------------------------------------

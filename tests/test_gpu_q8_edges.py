@@ -145,3 +145,49 @@ def test_hidden_pages_do_not_weigh_pages_without_values(new):
     c.vs[c.table[0, ::3]] = np.float32(2.0 ** -38)
     c.vs[c.table[0, 1::3]] = 0
     c.check(window=30)
+
+
+def _capped(c, cap, d=None):
+    """Outputs and bounds of a capped call; d: the scores' error, bound()'s without
+    a term for the cap where None."""
+    outs, tols, at = [], [], 0
+    for b, (n, m) in enumerate(zip(c.lens, c.new)):
+        k, v = (rows_of(x, s, c.table[b], n, c.code) for x, s in ((c.kc, c.ks), (c.vc, c.vs)))
+        o, mass, size = ref.attention(c.q[at:at + m].double().cpu().numpy(), k, v, 128 ** -0.5, cap)
+        if d is None:
+            tol = bound(o, mass, size, c.dtype)
+        else:
+            tol = 2.0 ** -23 * np.abs(o) + (2.0 ** -20 + 3.0 * d(size)) * mass
+        outs.append(o)
+        tols.append(tol + step_floor(c.vc, c.vs, c.table[b], n, c.code, c.heads, c.dtype))
+        at += m
+    return np.concatenate(outs), np.concatenate(tols)
+
+
+@pytest.mark.parametrize("cap", [50.0, 1e3, 1e6, 1e30, 3e38])
+@pytest.mark.parametrize("dtype,new", [("bf16", 1), ("bf16", 150), ("f32", 1), ("f32", 40)])
+def test_caps_of_any_size(cap, dtype, new):
+    """Scores of up to some 10 under caps of up to fp32's largest number, within the
+    bound of uncapped ones.  (A cap's own error is at most 2^-20 of the score, as in
+    the next test, and the bound's 2^-16 size holds 2^-17 size more than the sums.)"""
+    c = Case([400, 130], [min(new, 130)] * 2, 2, 4, ref.INT8, dtype, seed=35, gain=0.6)
+    got = c.run(cap=cap).double().cpu().numpy()
+    out, tol = _capped(c, cap)
+    assert (np.abs(got - out) <= tol).all()
+
+
+@pytest.mark.parametrize("cap", [0.5, 5.0, 50.0, 1e3, 1e4, 1e6])
+@pytest.mark.parametrize("new", [1, 40])
+def test_a_caps_error_goes_by_the_score(cap, new):
+    """fp32 queries of one element each, a power of two: scores without rounding
+    but for their scale (4 of 2^-24), the cap (2^-20: below half of it a polynomial
+    of 2^-22 and its roundings, else 1 - 2 / (1 + e^2t), off by some 4 of 2^-23 where
+    the cap is at most twice the score) and two products behind it: 2^-19 of the
+    score in all, and 2^-20 for the exponential and the value's scale."""
+    c = Case([400, 130], [new] * 2, 2, 4, ref.INT8, "f32", seed=36)
+    c.q.zero_()
+    at = torch.arange(c.q.shape[0] * c.heads, device="cuda").view(-1, c.heads, 1) * 37 % 128
+    c.q.scatter_(2, at, 64.0)          # scores within +-11
+    got = c.run(cap=cap).double().cpu().numpy()
+    out, tol = _capped(c, cap, d=lambda size: 2.0 ** -19 * size + 2.0 ** -20)
+    assert (np.abs(got - out) <= tol).all()
