@@ -178,9 +178,10 @@ __device__ __forceinline__ float2 split(uint64_t a) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
     return r;
 }
+// The largest of three, NaN if any is.
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 
@@ -513,7 +514,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
 #pragma unroll
                 for (int e = 0; e < kN; e += 2)
                     m[(e >> 1) & 3] = max3(m[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-                top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+                top = max3(m[0], m[1], max3(m[2], m[3], m[3]));
             }
             if (!(valued && settled)) {
                 if (!valued) {
@@ -592,7 +593,9 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&sh.p_full[i][n & 1]);
             const float2 s2 = split(sum2(sum0, sum1));   // (nobody waits for these)
-            l += (s2.x + s2.y) * isv;
+            // (a score that is NaN or +infinity, of a query that is not finite, makes the
+            // row NaN; ex2_poly would pass over it)
+            l = top < INFINITY ? l + (s2.x + s2.y) * isv : __int_as_float(0x7fffffff);
             if (left == 0) break;
             ++n;
         }

@@ -191,3 +191,51 @@ def test_a_caps_error_goes_by_the_score(cap, new):
     got = c.run(cap=cap).double().cpu().numpy()
     out, tol = _capped(c, cap, d=lambda size: 2.0 ** -19 * size + 2.0 ** -20)
     assert (np.abs(got - out) <= tol).all()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dtype,new", [("bf16", 1), ("f32", 5), ("bf16", 150)])
+@pytest.mark.parametrize("mod", [{}, dict(cap=20.0), dict(window=1)])
+def test_queries_that_are_not_finite_give_nan_in_their_rows(bad, dtype, new, mod):
+    """Wherever the row's keys lie (a first token sees one key only): NaN where the
+    formula gives NaN or +infinity for a score that it sees.  Scores that are all
+    finite (infinities under a cap are +-cap) give the formula's output, or NaN where
+    0 x infinity came into it; the other rows are as ever."""
+    c = Case([new, 500, 8 * 64 + 1], [new] * 3, 2, 4, ref.INT8, dtype, seed=40)
+    where = [(i, (3 * i) % c.heads) for i in range(0, 3 * new, 1 if new < 10 else 7)]
+    clean = c.q.clone()
+    for i, h in where:
+        c.q[i, h, (5 * i) % 128] = bad
+    q = c.q.double().cpu().numpy()
+    got = c.run(**mod).double().cpu().numpy()
+    c.q = clean
+    out, tol = c.want(**mod)
+    rows, sure = np.zeros(got.shape[:2], dtype=bool), 0
+    for i, h in where:
+        rows[i, h] = True
+        b, j = divmod(i, new)
+        k, v = (rows_of(x, s, c.table[b], c.lens[b], c.code)[:, h // 4] for x, s in ((c.kc, c.ks), (c.vc, c.vs)))
+        on = ref.visible(c.lens[b], new, mod.get("window", 0), 0)[j]
+        with np.errstate(all="ignore"):
+            x = 128 ** -0.5 * (k[on] @ q[i, h])
+            if "cap" in mod:
+                x = 20.0 * np.tanh(x / 20.0)
+        if not (x < np.inf).all():
+            sure += 1
+            assert np.isnan(got[i, h]).all()
+        elif np.isfinite(x).all():
+            w = np.exp(x - x.max())
+            w /= w.sum()
+            o, mass = w @ v[on], w @ np.abs(v[on])
+            near = np.abs(got[i, h] - o) <= bound(o, mass, np.full(1, 20.0), c.dtype, 20.0)
+            assert near.all() or np.isnan(got[i, h]).all()
+    assert sure or bad < 0 or "cap" in mod
+    assert (np.abs(got - out) <= tol)[~rows].all()
+
+
+@pytest.mark.parametrize("dtype,new", [("bf16", 4), ("f32", 4), ("bf16", 150)])
+def test_queries_that_are_not_finite_and_see_nothing_give_zeros(dtype, new):
+    c = Case([2, 90], [new, new], 2, 4, ref.INT8, dtype, seed=41)
+    c.q[0, 1, 2] = float("nan")
+    got = c.run()
+    assert (got[:new - 2] == 0).all() and torch.isfinite(got).all()
