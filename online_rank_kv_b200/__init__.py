@@ -377,18 +377,27 @@ def _launch(device: int, fn, where: str, *args, stream=None) -> None:
         raise IskvError(code, where)
 
 
-def _new_on(stream, make):
+def _new_on(stream, make, scratch=False):
     """make()'s tensors for a call on `stream` (None: the current one).  They
     come from that stream's pool, whose earlier work is done with the memory
     when the call runs, and go back to it only when the current stream, where
-    the caller reads them, has passed them too."""
+    the caller reads them, has passed them too (scratch: nobody does)."""
     if stream is None:
         return make()
     with torch.cuda.stream(stream):
         new = make()
-    for t in new:
-        t.record_stream(torch.cuda.current_stream(t.device))
+    if not scratch:
+        for t in new:
+            t.record_stream(torch.cuda.current_stream(t.device))
     return new
+
+
+def _hold(stream, *tensors) -> None:
+    """Keep the memory of a call's tensors (None among them) until `stream` has
+    passed the call, whatever the caller drops before."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def _int32(device: int, shape, t: torch.Tensor, name: str) -> int:
@@ -460,6 +469,8 @@ def page_plan(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, free: 
                        out_cu=((batch + 1,), out.cu), out_slots=((n,), out.slots), out_n_free=(one, out.n_free),
                        out_status=(one, out.status))
     args = _PlanArgs(batch, width, pages, n, *[t.data_ptr() for t in every])
+    if stream is not None:
+        _hold(stream, *every)
     _launch(dev, LIB.iskv_page_plan, "iskv_page_plan", ctypes.byref(args), stream=stream)
     return out
 
@@ -469,7 +480,10 @@ class Q8Pages:
     one scale per page and KV head.  ``k``, ``v`` [pages, kv_heads, 64, 128]
     (int8 or float8_e4m3fn) and ``k_scale``, ``v_scale`` [pages, kv_heads] are
     ordinary tensors; a stored row is codes * scale.  Requests take pages by
-    ``page_plan``.  Forward only."""
+    ``page_plan``.  Forward only.  Calls given a `stream` run there, hold their
+    tensors' memory until it has passed them, and leave it to the caller to order
+    the streams.  Rows that a call reads may have any token stride of at least a
+    row that is a multiple of 16 bytes."""
 
     def __init__(self, pages: int, kv_heads: int, code: int = CODE_INT8, device="cuda"):
         if code not in _CODE_DT:
@@ -504,6 +518,9 @@ class Q8Pages:
                            _ptr(v_scale))
         self._ref, self._status_at = ctypes.byref(self._c), self._status.data_ptr()
 
+    def _all(self):
+        return self.k, self.v, self.k_scale, self.v_scale, self._status
+
     def _rows(self, t: torch.Tensor, heads: int | None, name: str) -> int:
         shape = t.shape
         if len(shape) != 3 or shape[2] != 128 or (heads is not None and shape[1] != heads) \
@@ -517,24 +534,27 @@ class Q8Pages:
         return code
 
     def append(self, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
-        """Store rows k, v [n, kv_heads, 128] (any token stride) in the slots
-        [n] that ``page_plan`` gave; rows with slot -1 are skipped."""
+        """Store rows k, v [n, kv_heads, 128] in the slots [n] that
+        ``page_plan`` gave; rows with slot -1 are skipped."""
         dt = self._rows(k, self.kv_heads, "k")
         if (k.requires_grad or v.requires_grad) and torch.is_grad_enabled():
             raise ValueError("8-bit pages are forward only: detach k and v")
         if self._rows(v, self.kv_heads, "v") != dt or v.shape != k.shape:
             raise ValueError("k and v must agree in shape and type")
         n = k.shape[0]
+        at = _int32(self._dev, (n,), slots, "slots")
+        if stream is not None:
+            _hold(stream, k, v, slots, *self._all())
         _launch(self._dev, LIB.iskv_q8_append, "iskv_q8_append", self._ref, k.data_ptr(), v.data_ptr(), dt, k.stride(0),
-                v.stride(0), n, _int32(self._dev, (n,), slots, "slots"), self._status_at, stream=stream)
+                v.stride(0), n, at, self._status_at, stream=stream)
 
     def attention(self, q: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, cu: torch.Tensor, max_new: int,
                   scale: float = 128 ** -0.5, cap: float = 0.0, slopes: torch.Tensor | None = None,
                   window: int = 0, prefix: torch.Tensor | None = None, out: torch.Tensor | None = None,
                   stream=None) -> torch.Tensor:
-        """Attention of q [tokens, q_heads, 128] (any token stride): request
-        b's queries are rows cu[b]:cu[b+1] and the last of its lens[b] stored
-        tokens.  Causal; `window` > 0 limits how far back a query sees,
+        """Attention of q [tokens, q_heads, 128]: request b's queries are rows
+        cu[b]:cu[b+1] and the last of its lens[b] stored tokens.  Causal;
+        `window` > 0 limits how far back a query sees,
         prefix[b] tokens at the start are seen by all; `cap` caps scores by
         cap*tanh(x/cap); slopes[q_heads] (fp32) take slope * distance off.
         `max_new` is the largest number of queries of one request.  Returns
@@ -560,7 +580,7 @@ class Q8Pages:
                 need = LIB.iskv_q8_workspace(heads, self.kv_heads, n, max_new, dt)
             if len(self._need) < 64:
                 self._need[(heads, max_new, dt)] = need
-        ws, = _new_on(stream, lambda: (q.new_empty(max(need, 0), dtype=torch.uint8),))
+        ws, = _new_on(stream, lambda: (q.new_empty(max(need, 0), dtype=torch.uint8),), scratch=True)
         i32 = torch.int32
         if not (table.dtype is i32 and lens.dtype is i32 and cu.dtype is i32 and cu.numel() == batch + 1
                 and table.get_device() == dev and lens.get_device() == dev and cu.get_device() == dev
@@ -570,8 +590,8 @@ class Q8Pages:
                             out.data_ptr(), table.data_ptr(), lens.data_ptr(), cu.data_ptr(),
                             None if prefix is None else _int32(dev, (batch,), prefix, "prefix"),
                             None if slopes is None else slopes.data_ptr(), ws.data_ptr(), need, self._status_at)
-        if stream is not None:   # (an out of the caller's may be the current stream's)
-            out.record_stream(stream)
+        if stream is not None:
+            _hold(stream, q, out, table, lens, cu, prefix, slopes, *self._all())
         _launch(dev, LIB.iskv_q8_attention, "iskv_q8_attention", self._ref, ctypes.byref(args), stream=stream)
         return out
 

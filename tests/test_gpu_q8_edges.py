@@ -239,3 +239,65 @@ def test_queries_that_are_not_finite_and_see_nothing_give_zeros(dtype, new):
     c.q[0, 1, 2] = float("nan")
     got = c.run()
     assert (got[:new - 2] == 0).all() and torch.isfinite(got).all()
+
+
+def test_inputs_dropped_after_a_call_on_another_stream():
+    """A call on a given stream holds its inputs until that stream has passed it:
+    what the current stream allocates next does not get their memory before."""
+    import online_rank_kv_b200 as ik
+    gen = torch.Generator(device="cuda").manual_seed(43)
+    n, kv, heads = 300, 2, 8
+    make = lambda h, dt: torch.randn(n, h, 128, generator=gen, device="cuda").to(dt)
+    k, v, q = make(kv, torch.float32), make(kv, torch.float32), make(heads, torch.bfloat16)
+    table, slots = _i32([[4, 2, 0, 1, 3]]), _i32([64 * [4, 2, 0, 1, 3][t // 64] + t % 64 for t in range(n)])
+    lens, cu, prefix, add = _i32([n]), _i32([0, n]), _i32([20]), _i32([n])
+    slopes = torch.full((heads,), 0.25, device="cuda")
+    free, n_free = _i32([3, 1, 0, 2, 4]), _i32([5])
+
+    def run(stream, copies):
+        pages = ik.Q8Pages(5, kv)
+        state = torch.full((1, 5), -1, dtype=torch.int32, device="cuda"), free.clone(), n_free.clone()
+        out, plan = torch.zeros_like(q), ik.PagePlan.empty(1, n)
+        torch.cuda.synchronize()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(40_000_000)          # some 20 ms
+        hold = []
+
+        def dropped(*tensors):
+            """Fresh copies of a call's inputs; the ones of the call before go."""
+            here = [t.clone() for t in tensors]
+            if copies:
+                torch.cuda.current_stream().synchronize()
+            else:
+                hold.append(here)
+            return here
+        ik.page_plan(*dropped(0 * lens, add), *state, out=plan, stream=stream)
+        junk = [torch.full_like(t, 9) for t in (lens, add) for _ in range(4)]
+        pages.append(*dropped(k, v, slots), stream=stream)
+        junk += [torch.full_like(t, 9) for t in (k, v, slots) for _ in range(4)]
+        a = dropped(q, table, lens, cu, prefix, slopes)
+        pages.attention(*a[:4], max_new=n, prefix=a[4], slopes=a[5], out=out, stream=stream)
+        del a
+        junk += [torch.full_like(t, 9) for t in (q, table, lens, cu, prefix, slopes) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert pages.status() == 0 and plan.status.item() == 0
+        return pages.k, pages.k_scale, pages.v, out, plan.lens, plan.slots, state[0]
+    want = run(None, False)
+    got = run(torch.cuda.Stream(), True)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
+def test_pages_dropped_after_a_call_on_another_stream():
+    import online_rank_kv_b200 as ik
+    side, pages = torch.cuda.Stream(), ik.Q8Pages(200, 8)
+    x, slots = torch.randn(12800, 8, 128, device="cuda"), _i32(np.arange(12800))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(40_000_000)
+    pages.append(x, x, slots, stream=side)
+    del pages
+    junk = [torch.full((200, 8, 64, 128), 9, dtype=torch.int8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all((j == 9).all() for j in junk)
