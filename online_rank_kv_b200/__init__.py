@@ -596,7 +596,9 @@ class Q8Pages:
         return out
 
     def status(self) -> int:
-        """Synchronize and return the sticky status of the calls on these pages:
+        """Synchronize the device and return the sticky status of the calls on
+        these pages, whichever streams they ran on:
         0, or the smallest code of non-finite rows (RANGE), a device-side wait
         that gave up (DEVICE_TIMEOUT) and slots outside the pool (INVALID_ARG)."""
+        torch.cuda.synchronize(self._dev)
         return int(self._status.item())

@@ -301,3 +301,17 @@ def test_pages_dropped_after_a_call_on_another_stream():
     junk = [torch.full((200, 8, 64, 128), 9, dtype=torch.int8, device="cuda") for _ in range(4)]
     torch.cuda.synchronize()
     assert all((j == 9).all() for j in junk)
+
+
+def test_status_waits_for_calls_on_other_streams():
+    import online_rank_kv_b200 as ik
+    side, pages = torch.cuda.Stream(), ik.Q8Pages(2, 2)
+    x, slots = torch.zeros(3, 2, 128, device="cuda"), _i32([0, 1, 2])
+    pages.append(x, x, slots)                  # (the kernel is loaded before the wait begins)
+    assert pages.status() == 0
+    x.fill_(float("nan"))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)         # some 100 ms
+    pages.append(x, x, slots, stream=side)
+    assert pages.status() == -9
