@@ -469,8 +469,9 @@ typedef struct {
  * Elements that are not finite are stored as zeros and set *status to
  * ISKV_ERR_RANGE; slots outside -1 .. 64*pages-1 are skipped and set it to
  * ISKV_ERR_INVALID_ARG (the smaller code stays; *status is otherwise left;
- * NULL: not reported).  k and v must be 16-byte aligned, strides multiples of
- * 16 bytes.  Errors: INVALID_ARG, UNSUPPORTED (head_dim, page), CUDA.        */
+ * NULL: not reported).  k and v must be 16-byte aligned, the strides of several
+ * rows multiples of 16 bytes and at least a row.
+ * Errors: INVALID_ARG, UNSUPPORTED (head_dim, page), CUDA.                  */
 ISKV_API int iskv_q8_append(const iskv_q8_pages* store, const void* k, const void* v, int dtype,
                             int64_t k_stride, int64_t v_stride, int64_t n, const int32_t* slots,
                             int32_t* status, void* stream);
@@ -503,7 +504,8 @@ ISKV_API int iskv_q8_append(const iskv_q8_pages* store, const void* k, const voi
  * A query row is read by several blocks, so out may not overlap q's rows or the
  * space between them (INVALID_ARG).
  * q_heads / kv_heads <= 8; ISKV_BF16 or ISKV_F32 queries; q, out and
- * workspace 16-byte aligned, q_stride a multiple of 16 bytes.
+ * workspace 16-byte aligned, q_stride (of several tokens) a multiple of 16 bytes
+ * and at least a row.
  * Errors: INVALID_ARG, UNSUPPORTED (head_dim, page, heads per group),
  * CAPACITY (workspace too small), CUDA.                                     */
 typedef struct {

@@ -141,7 +141,7 @@ int iskv_q8_append(const iskv_q8_pages* store, const void* k, const void* v, int
     if (!k || !v || !slots || !aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4) || !aligned(status, 4))
         return ISKV_ERR_INVALID_ARG;
     for (int64_t st : {k_stride, v_stride})
-        if (st % per16 != 0 || (n > 1 && st < row)) return ISKV_ERR_INVALID_ARG;
+        if (n > 1 && (st % per16 != 0 || st < row)) return ISKV_ERR_INVALID_ARG;   // (a single row has no next one)
     const void* ptrs[] = {store->k, store->v, store->k_scale, store->v_scale, k, v, slots, status};
     if (!all_on_device(ptrs, 8)) return ISKV_ERR_INVALID_ARG;
     q8::AppendArgs a{};
@@ -192,8 +192,8 @@ int iskv_q8_attention(const iskv_q8_pages* store, const iskv_q8_attention_args* 
     if (!aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->workspace, 16) || !aligned(a->table, 4) ||
         !aligned(a->lens, 4) || !aligned(a->cu, 4) || !aligned(a->prefix, 4) || !aligned(a->slopes, 4) || !aligned(a->status, 4))
         return ISKV_ERR_INVALID_ARG;
-    if (a->q_stride % (16 / elem_bytes(a->dtype)) != 0 ||
-        (a->tokens > 1 && a->q_stride < (int64_t)a->q_heads * kHeadDim))
+    if (a->tokens > 1 &&
+        (a->q_stride % (16 / elem_bytes(a->dtype)) != 0 || a->q_stride < (int64_t)a->q_heads * kHeadDim))
         return ISKV_ERR_INVALID_ARG;
     const int64_t row = (int64_t)a->q_heads * kHeadDim, es = elem_bytes(a->dtype);
     if (overlap(a->q, ((a->tokens - 1) * a->q_stride + row) * es, a->out, a->tokens * row * es)) return ISKV_ERR_INVALID_ARG;

@@ -315,3 +315,28 @@ def test_status_waits_for_calls_on_other_streams():
         torch.cuda._sleep(200_000_000)         # some 100 ms
     pages.append(x, x, slots, stream=side)
     assert pages.status() == -9
+
+
+@pytest.mark.parametrize("kv_heads", [1, 2])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_row_whatever_its_token_stride(kv_heads, dtype):
+    """A single row has no next one: its token stride is whatever a view left."""
+    import online_rank_kv_b200 as ik
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    gen = torch.Generator(device="cuda").manual_seed(42)
+    k, v = [torch.randn(1, kv_heads, 128, generator=gen, device="cuda").to(dt) for _ in range(2)]
+    q = torch.randn(1, 2 * kv_heads, 128, generator=gen, device="cuda").to(dt)
+    slots, table, lens, cu = _i32([64]), _i32([[1]]), _i32([1]), _i32([0, 1])
+
+    def odd(x):
+        y = torch.as_strided(x, x.shape, (1, 128, 1))
+        assert y.stride(0) == 1
+        return y
+    got = []
+    for f in (lambda x: x, odd):
+        store = ik.Q8Pages(2, kv_heads)
+        store.append(f(k), f(v), slots)
+        got.append((store.k.clone(), store.v.clone(), store.attention(f(q), table, lens, cu, max_new=1)))
+        assert store.status() == 0
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
