@@ -36,8 +36,8 @@ template <>
 struct Raw<float> {
     float4 a, b;
     __device__ __forceinline__ void load(const float* p) {
-        a = __ldg(reinterpret_cast<const float4*>(p));
-        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        a = *reinterpret_cast<const float4*>(p);
+        b = reinterpret_cast<const float4*>(p)[1];
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
     // the largest magnitude's fp32 bits: they order like the values, with
@@ -57,7 +57,7 @@ struct Raw<float> {
 template <>
 struct Raw<__nv_bfloat16> {
     uint4 a;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
     __device__ __forceinline__ uint32_t top() const {
         const uint32_t k = 0x7fff7fffu;

@@ -358,7 +358,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
 #pragma unroll
         for (int z = 0; z < 16; ++z) {
             const int64_t src = __shfl_sync(0xffffffffu, own, 2 * z + up16);
-            x[z] = src >= 0 ? __ldg(reinterpret_cast<const uint4*>(q0 + src)) : make_uint4(0u, 0u, 0u, 0u);
+            x[z] = src >= 0 ? *reinterpret_cast<const uint4*>(q0 + src) : make_uint4(0u, 0u, 0u, 0u);
         }
     };
     {
@@ -786,11 +786,11 @@ __device__ __forceinline__ void walk_role(const AttnArgs& p, Shared& sh, int sta
             if (in == 0) {   // pages and scales of 32 steps, one per lane
                 const int j = i + lane;
                 const int tok = w.span.step_of(j) * kN;
-                page = j < w.t1 && tok < w.r.len ? __ldg(p.table + (int64_t)w.b * p.width + tok / kPage) : -1;
+                page = j < w.t1 && tok < w.r.len ? p.table[(int64_t)w.b * p.width + tok / kPage] : -1;
                 if (page >= p.pages) page = -1;
                 const int64_t at = (int64_t)max(page, 0) * p.kv_heads + w.h;
-                sk = page >= 0 ? __ldg(p.k_scale + at) : 0.f;
-                const float sv = page >= 0 ? __ldg(p.v_scale + at) : 0.f;
+                sk = page >= 0 ? p.k_scale[at] : 0.f;
+                const float sv = page >= 0 ? p.v_scale[at] : 0.f;
                 lsv = lg2(sv);
                 isv = sv > 0.f ? __fdividef(1.f, sv) : 0.f;
             }

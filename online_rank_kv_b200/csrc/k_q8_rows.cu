@@ -432,14 +432,14 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
                         const float4* f4 = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + src);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const float4 v = on ? __ldg(f4 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                            const float4 v = on ? f4[i] : make_float4(0.f, 0.f, 0.f, 0.f);
                             x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
                         }
                     } else {
                         const uint4* u4 = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + src);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const uint4 v = on ? __ldg(u4 + i) : make_uint4(0u, 0u, 0u, 0u);
+                            const uint4 v = on ? u4[i] : make_uint4(0u, 0u, 0u, 0u);
                             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
@@ -514,8 +514,8 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
                 __syncwarp();
             }
             const int64_t block = (int64_t)max(this_page, 0) * p.kv_heads + at.h;
-            const float sk = __ldg(p.k_scale + block);
-            const float sv = __ldg(p.v_scale + block);
+            const float sk = p.k_scale[block];
+            const float sv = p.v_scale[block];
             const uint32_t kb = ring_at + stage * kStageBytes, vb = kb + kStoreBytes;
             stage = stage + 1 == kStages ? 0 : stage + 1;
 

@@ -38,7 +38,8 @@ struct SmemOnce {
 
 // Launches a kernel that may come up while the one before it in the stream ends.
 // It calls after_previous() before it touches memory, which waits for that
-// kernel's end and its writes; kernels but the joins call let_next() at once, so
+// kernel's end and its writes.  (What it reads may be written until then, so none
+// of it is read-only for the kernel's whole life, as __ldg would ask.)  Kernels but the joins call let_next() at once, so
 // that what follows them need not wait for its own launch. (A grid that is up
 // while a join's many blocks run slows them by more than its launch.) A page plan and eight layers of
 // append and attention, 1000 keys a request: batch 1 119 -> 113 us as a graph,

@@ -340,3 +340,42 @@ def test_one_row_whatever_its_token_stride(kv_heads, dtype):
         assert store.status() == 0
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("new,code", [(1, ref.INT8), (1, ref.E4M3), (40, ref.INT8), (40, ref.E4M3)])
+def test_each_call_reads_what_the_one_before_wrote(new, code):
+    """Page plan, append and attention with nothing between them, again and again:
+    the queries and rows are the attention's last output, the table, lengths and
+    slots the plan's, and the pages' scales grow at every step.  The same bits as
+    with a synchronize after every call."""
+    import online_rank_kv_b200 as ik
+    batch, steps, heads = 2, 25, 4
+    n = batch * new
+
+    def run(sync):
+        pages = ik.Q8Pages(40, heads, code)
+        table, free, plan = _i32(np.full((batch, 20), -1)), _i32(np.arange(40)), ik.PagePlan.empty(batch, n)
+        plan.lens.zero_()
+        plan.n_free.fill_(40)
+        add = _i32([new] * batch)
+        gen = torch.Generator(device="cuda").manual_seed(44)
+        x = [torch.randn(n, heads, 128, generator=gen, device="cuda").bfloat16() for _ in range(2)]
+        rows = [torch.randn(n, heads, 128, generator=gen, device="cuda").bfloat16() * 1.3 ** i for i in range(steps)]
+        torch.cuda.synchronize()
+        for i in range(steps):
+            ik.page_plan(plan.lens, add, table, free, plan.n_free, out=plan)
+            sync()
+            pages.append(rows[i], x[i % 2], plan.slots)
+            sync()
+            pages.attention(x[i % 2], table, plan.lens, plan.cu, max_new=new, scale=0.05, out=x[(i + 1) % 2])
+            sync()
+            pages.append(x[(i + 1) % 2], rows[i], plan.slots)      # the same tokens once more
+            sync()
+        torch.cuda.synchronize()
+        assert pages.status() == 0 and plan.status.item() == 0
+        return x + [pages.k.view(torch.uint8), pages.v.view(torch.uint8), pages.k_scale, pages.v_scale]
+    want = run(torch.cuda.synchronize)
+    assert all(torch.isfinite(w).all() for w in want[:2])
+    for _ in range(5):
+        for a, b in zip(run(lambda: None), want):
+            assert torch.equal(a, b)
