@@ -76,9 +76,8 @@ constexpr int kPolyOf4 = 1;
 constexpr int kPieceSteps = 6;
 
 // One step, as the walking warp describes it.
-constexpr int kFirst = 1, kEnd = 2;     // of a piece; of the work
 struct Step {
-    int flags, key0;
+    int end, key0;          // end: of the work, nothing else holds then
     int left;               // steps of the piece that follow
     int page;               // -1: there is none
     float sk, lsv, isv;     // key scale, log2 of the value scale, its inverse (0: a page of scale 0)
@@ -363,7 +362,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
     };
     {
         const bool ok = wait_for(p, sh, &sh.info_full[0], 0);
-        if (!ok || (sh.step[0].flags & kEnd)) return;
+        if (!ok || sh.step[0].end) return;
         load(sh.step[0]);
     }
 
@@ -611,7 +610,7 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
         const int last = n++;
         bool ok = wait_for(p, sh, &sh.info_full[n % kSteps], (n / kSteps) & 1);
         if (!ok) return;
-        more = !(sh.step[n % kSteps].flags & kEnd);
+        more = !sh.step[n % kSteps].end;
         if (more) load(sh.step[n % kSteps]);
         ok = wait_for(p, sh, &sh.pv_done[i][last & 1], (last >> 1) & 1);
         if (!ok) return;
@@ -656,7 +655,7 @@ __device__ __forceinline__ void code_role(const AttnArgs& p, Shared& sh, uint8_t
         bool ok = lane_wait(p, sh, &sh.info_full[n % kSteps], (n / kSteps) & 1);
         const int rows = st.page >= 0 ? st.len - st.key0 : 0;
         const bool valued = st.isv > 0.f;   // (what scale 0 multiplies is nothing, whatever the codes)
-        if (!__all_sync(0xffffffffu, ok && !(st.flags & kEnd))) return;
+        if (!__all_sync(0xffffffffu, ok && !st.end)) return;
         if (lane == 0) tc::mbar_arrive(&sh.info_empty[n % kSteps]);
         const int bf = n % kBuffers;
 #pragma unroll 1
@@ -715,7 +714,7 @@ __device__ __forceinline__ void mma_role(const AttnArgs& p, Shared& sh, uint32_t
     bool ok = true;
     for (int n = 0, piece = 0; ok; ++piece) {
         ok = waited(&sh.info_full[n % kSteps], (n / kSteps) & 1);
-        if (!ok || uniform(sh.step[n % kSteps].flags & kEnd)) break;
+        if (!ok || uniform(sh.step[n % kSteps].end)) break;
         int ahead = 0;                     // steps of the piece whose scores are on their way
         const int steps = uniform(sh.step[n % kSteps].left) + 1;
         ok = waited(&sh.q_full[i], piece & 1);
@@ -798,7 +797,7 @@ __device__ __forceinline__ void walk_role(const AttnArgs& p, Shared& sh, int sta
             if (!ok) break;
             if (lane == in) {
                 Step& st = sh.step[n % kSteps];
-                st.flags = i == w.t0 ? kFirst : 0;
+                st.end = 0;
                 st.key0 = w.span.step_of(i) * kN;
                 st.left = w.t1 - 1 - i;
                 st.page = page;
@@ -821,7 +820,7 @@ __device__ __forceinline__ void walk_role(const AttnArgs& p, Shared& sh, int sta
     if (ok) {
         ok = wait_for(p, sh, &sh.info_empty[n % kSteps], ((n / kSteps) & 1) ^ 1);
         if (ok && lane == 0) {
-            sh.step[n % kSteps].flags = kEnd;
+            sh.step[n % kSteps].end = 1;
             tc::mbar_arrive(&sh.info_full[n % kSteps]);
         }
     }
@@ -832,7 +831,7 @@ __device__ __forceinline__ void copy_role(const AttnArgs& p, Shared& sh, uint8_t
     bool ok = true;
     for (int n = 0;; ++n) {
         ok = wait_for(p, sh, &sh.info_full[n % kSteps], (n / kSteps) & 1);
-        if (!ok || (sh.step[n % kSteps].flags & kEnd)) break;
+        if (!ok || sh.step[n % kSteps].end) break;
         const int page = sh.step[n % kSteps].page;
         const int64_t at = ((int64_t)max(page, 0) * p.kv_heads + sh.step[n % kSteps].h) * kCodeBytes;
         __syncwarp();
