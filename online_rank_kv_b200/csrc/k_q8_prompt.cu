@@ -486,14 +486,27 @@ __device__ __forceinline__ void softmax_role(const AttnArgs& p, Shared& sh, uint
             tmem_wait(*reinterpret_cast<uint32_t(*)[32]>(s));
             tmem_wait(*reinterpret_cast<uint32_t(*)[32]>(s + 32));
             if (MOD) {
-                const float d0 = (float)(pos - key0);
+                // (each choice once for all keys: made key by key they cost more than the work)
+                if (p.cap > 0.f) {
+                    float far = 0.f;
 #pragma unroll
-                for (int e = 0; e < kN; ++e) {
-                    float y = __uint_as_float(s[e]) * a;
-                    if (p.cap > 0.f) y = capped(y, p.cap, p.cap_inv);
-                    s[e] = __float_as_uint(y * kLog2e - slope * fabsf(d0 - (float)e));
+                    for (int e = 0; e < kN; ++e) far = fmaxf(far, fabsf(__uint_as_float(s[e])));
+                    if (__all_sync(0xffffffffu, far * a * p.cap_inv < kCapLow)) {
+#pragma unroll
+                        for (int e = 0; e < kN; ++e) s[e] = __float_as_uint(capped_low(__uint_as_float(s[e]) * a, p.cap_inv));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < kN; ++e) s[e] = __float_as_uint(capped(__uint_as_float(s[e]) * a, p.cap, p.cap_inv));
+                    }
+                    a = 1.f;
                 }
-                a = 1.f;
+                a *= kLog2e;
+                if (p.slopes) {
+                    const float d0 = (float)(pos - key0);
+#pragma unroll
+                    for (int e = 0; e < kN; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * a - slope * fabsf(d0 - (float)e));
+                    a = 1.f;
+                }
             }
             if (!clear) {
 #pragma unroll

@@ -171,13 +171,18 @@ __device__ __forceinline__ float lg2(float x) {
 // above x; from there on cap (1 - 2 / (1 + e^(2t))), whose error of a few 2^-23 of
 // the cap is one of 2^-21 of tanh there, and whose limits are exact (e^(2t)
 // reaches 0 and infinity).
-__device__ __forceinline__ float capped(float x, float cap, float inv) {
+constexpr float kCapLow = 0.5f;
+__device__ __forceinline__ float capped_low(float x, float inv) {
     const float t = x * inv, u = t * t;
     float y = fmaf(0.01724136434495449f, u, -0.05304544046521187f);
     y = fmaf(y, u, 0.13325878977775574f);
     y = fmaf(y, u, -0.333331435918808f);
-    y = x * fmaf(y, u, 1.f);
-    if (!(fabsf(t) < 0.5f)) y = cap * (1.f - __fdividef(2.f, 1.f + ex2(2.f * kLog2e * t)));
+    return x * fmaf(y, u, 1.f);
+}
+__device__ __forceinline__ float capped(float x, float cap, float inv) {
+    const float t = x * inv;
+    float y = capped_low(x, inv);
+    if (!(fabsf(t) < kCapLow)) y = cap * (1.f - __fdividef(2.f, 1.f + ex2(2.f * kLog2e * t)));
     return y;
 }
 

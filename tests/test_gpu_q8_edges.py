@@ -379,3 +379,16 @@ def test_each_call_reads_what_the_one_before_wrote(new, code):
     for _ in range(5):
         for a, b in zip(run(lambda: None), want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("code", [ref.INT8, ref.E4M3])
+@pytest.mark.parametrize("cap", [0.25, 2.0, 8.0])
+@pytest.mark.parametrize("dtype,new", [("bf16", 1), ("bf16", 150), ("f32", 9)])
+def test_caps_that_bind(code, cap, dtype, new):
+    """Scores on both sides of half the cap and far above it."""
+    c = Case([400, 1300], [new, new], 2, 4, code, dtype, seed=45, gain=0.6)
+    c.q[::3] *= 0.05
+    c.q[1::3] *= 4.0
+    got = c.run(cap=cap).double().cpu().numpy()
+    out, tol = _capped(c, cap)
+    assert (np.abs(got - out) <= tol).all()
