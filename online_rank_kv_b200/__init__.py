@@ -412,6 +412,9 @@ def _all_int32(device: int, **tensors) -> None:
         _int32(device, shape, t, name)
 
 
+_I31 = 2 ** 31
+
+
 def _on_cuda(t: torch.Tensor, name: str) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
@@ -458,6 +461,8 @@ def page_plan(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, free: 
             raise ValueError("tokens (the number of slots) or out is needed")
         out = PagePlan(*_new_on(stream, lambda: PagePlan.empty(batch, tokens, lens.device)._all()))
     n, pages = out.slots.shape[0], free.shape[0]
+    if max(n, width, pages) >= _I31:
+        raise ValueError("slots, table columns and pages must be fewer than 2^31")
     every = (lens, add, table, free, n_free, out.lens, out.cu, out.slots, out.n_free, out.status)
     sizes = (batch, batch, batch * width, pages, 1, batch, batch + 1, n, 1, 1)
     i32 = torch.int32
@@ -558,7 +563,8 @@ class Q8Pages:
         prefix[b] tokens at the start are seen by all; `cap` caps scores by
         cap*tanh(x/cap); slopes[q_heads] (fp32) take slope * distance off.
         `max_new` is the largest number of queries of one request.  Returns
-        out [tokens, q_heads, 128] in q's type."""
+        out [tokens, q_heads, 128] in q's type; its rows from cu[batch] on are
+        left as they were (of a new out: anything)."""
         dt = self._rows(q, None, "q")
         n, heads = q.shape[0], q.shape[1]
         dev = self._dev
@@ -571,6 +577,8 @@ class Q8Pages:
         if lens.dim() != 1 or table.dim() != 2:
             raise ValueError("lens must be 1-d, table 2-d")
         batch, width = lens.shape[0], table.shape[1]
+        if not (-_I31 <= window < _I31 and -_I31 <= max_new < _I31 and width < _I31):
+            raise ValueError("window, max_new and the table's columns must be 32-bit numbers")
         if slopes is not None and (slopes.dtype != torch.float32 or tuple(slopes.shape) != (heads,)
                                    or slopes.get_device() != dev or not slopes.is_contiguous()):
             raise ValueError("slopes must be a contiguous fp32 tensor [q_heads] on the pages' device")

@@ -392,3 +392,75 @@ def test_caps_that_bind(code, cap, dtype, new):
     got = c.run(cap=cap).double().cpu().numpy()
     out, tol = _capped(c, cap)
     assert (np.abs(got - out) <= tol).all()
+
+
+def test_numbers_beyond_32_bits_are_refused():
+    """A window or a largest number of queries that the library's int32 would cut."""
+    import online_rank_kv_b200 as ik
+    store = ik.Q8Pages(2, 2)
+    x = torch.ones(100, 2, 128, device="cuda")
+    store.append(x, x, _i32(np.arange(100)))
+    q, args = torch.ones(1, 4, 128, device="cuda"), (_i32([[0, 1]]), _i32([100]), _i32([0, 1]))
+    for kw in (dict(window=2 ** 32 + 5), dict(window=2 ** 31), dict(max_new=2 ** 32 + 1), dict(max_new=2 ** 31),
+               dict(window=-2 ** 32)):
+        with pytest.raises(ValueError):
+            store.attention(q, *args, **dict(dict(max_new=1), **kw))
+    a = store.attention(q, *args, max_new=1, window=2 ** 31 - 1)
+    assert torch.equal(a, store.attention(q, *args, max_new=1))
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_calls_on_given_streams_inside_a_capture(new):
+    """A captured step whose calls name their streams, one of them forked off the
+    capturing one, with temporary inputs: replayed with other lengths and rows, it
+    gives what eager calls give."""
+    import online_rank_kv_b200 as ik
+    batch, kv, heads = 3, 2, 8
+    n = batch * new
+    gen = torch.Generator(device="cuda").manual_seed(46)
+
+    class State:
+        def __init__(self):
+            self.table, self.free = _i32(np.full((batch, 12), -1)), _i32(np.arange(40))
+            self.plan = ik.PagePlan.empty(batch, n)
+            self.plan.lens.zero_()
+            self.plan.n_free.fill_(40)
+            self.add = _i32([new] * batch)
+            self.pages = ik.Q8Pages(40, kv, ik.CODE_E4M3)
+            self.x = torch.zeros(n, heads + 2 * kv, 128, device="cuda", dtype=torch.bfloat16)
+            self.out = torch.zeros(n, heads, 128, device="cuda", dtype=torch.bfloat16)
+
+        def step(self, side):
+            here = torch.cuda.current_stream()
+            ik.page_plan(self.plan.lens, self.add, self.table, self.free, self.plan.n_free, out=self.plan, stream=here)
+            k = self.x[:, heads:heads + kv] * 2
+            if side is not None:
+                side.wait_stream(here)
+            self.pages.append(k, self.x[:, heads + kv:], self.plan.slots, stream=side)
+            q = self.x[:, :heads] + 0
+            if side is not None:
+                side.wait_stream(here)
+            got = self.pages.attention(q, self.table, self.plan.lens, self.plan.cu, max_new=new, stream=side)
+            if side is not None:
+                here.wait_stream(side)
+            self.out.copy_(got)
+    eager, captured, side = State(), State(), torch.cuda.Stream()
+    captured.add.zero_()
+    captured.step(None)
+    captured.add.fill_(new)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured.step(side)
+    for i in range(8):
+        x = torch.randn(eager.x.shape, generator=gen, device="cuda").bfloat16()
+        for s in (eager, captured):
+            s.x.copy_(x)
+            s.add.copy_(_i32([new, i % 2, 0]))
+        eager.step(None)
+        graph.replay()
+        torch.cuda.synchronize()
+        m = int(eager.plan.cu[-1])
+        assert torch.equal(eager.plan.lens, captured.plan.lens) and torch.equal(eager.plan.slots, captured.plan.slots)
+        assert torch.equal(eager.out[:m], captured.out[:m])
+        assert torch.equal(eager.pages.k.view(torch.uint8), captured.pages.k.view(torch.uint8))
+    assert captured.pages.status() == 0 and captured.plan.status.item() == 0
