@@ -492,7 +492,8 @@ ISKV_API int iskv_q8_append(const iskv_q8_pages* store, const void* k, const voi
  * prefix that every query of the request sees whole.  One softmax over what
  * it sees; out ([tokens][q_heads][128], contiguous, in dtype) is the weighted
  * sum of V, zeros where a query sees nothing (lens[b] smaller than the number
- * of its queries).  Rows of out from cu[batch] on are left as they were.
+ * of its queries), NaN where a score that it sees is NaN or +infinity (queries
+ * that are not finite).  Rows of out from cu[batch] on are left as they were.
  * `max_new` tells the host the largest number of queries of one request (it
  * picks the kernel; a wrong value costs time, not results).  A page number
  * outside 0..pages-1 hides its tokens; lens is taken as at most 64 * width.

@@ -81,15 +81,17 @@ long long wait_cycles() {
 
 // Row tiles of the split kernel in eights of rows.  Several tiles of a request
 // read the same keys from L2, and one tile's code is the faster: two pay only for
-// long fp32 prompts (6 requests of 9000 tokens, 3 heads a group: 48 rows 48 us
-// against 51 with two, 192 rows 137 against 106).
+// long fp32 prompts (6 requests of 9000 tokens, 3 heads a group: 2 KV heads: 48 rows
+// 48 us either way, 192 rows 142 against 103; 8 KV heads: 148 against 122 and 528
+// against 339).
 int row_tiles8(int g, int max_new, int dtype) { return dtype == ISKV_F32 && (int64_t)max_new * g > 64 ? 2 : 1; }
 
 // Whether the split kernel gives whole (request, head, tile) items to its CTAs,
 // so that no second launch has to join parts: where requests are very short, or
 // short and many.  (8 KV heads, requests as long as the table; one launch
-// against two: 1 request of 64 tokens 8.9 us against 11.2, of 512 14.8 against
-// 11.9; 64 requests of 512 26.6 against 28.5, ragged ones of up to 1024 36 against 34.)
+// against two, when the rule was chosen: 1 request of 64 tokens 8.9 us against 11.2,
+// of 512 14.8 against 11.9; 64 requests of 512 26.6 against 28.5, ragged ones of up
+// to 1024 36 against 34; with the rule now 8.8, 12.1, 28.3 and 34.4.)
 bool whole_items(int width, int batch, int kv_heads, int ctas) {
     return width <= 2 || (width <= 8 && (int64_t)batch * kv_heads >= 2 * (int64_t)ctas);
 }
@@ -103,8 +105,8 @@ int64_t prompt_floats(int ctas) { return (int64_t)ctas * 2 * q8::kPromptRows * (
 // Query rows per KV head up to which the split kernel takes a request: the
 // tcgen05 kernel turns every code into an operand whatever the rows, the split
 // kernel goes over the codes once per 8 rows (8 KV heads, 4 heads a group,
-// 16K tokens: 32 rows 39 us in both, 64 rows 57 against 40; 32 requests of 8K
-// tokens: 241 against 272 and 388 against 273).
+// 16K tokens: 32 rows 38 us against 40, 64 rows 57 against 41; 32 requests of 8K
+// tokens: 234 against 277 and 406 against 278).
 constexpr int64_t kPromptMinRows = 32;
 
 bool is_prompt(int g, int max_new, int dtype) { return dtype == ISKV_BF16 && (int64_t)max_new * g > kPromptMinRows; }

@@ -16,7 +16,7 @@
 // and the product is the quotient.
 //
 // Bound by DRAM for prompts (3 bytes per bf16 element: 16K tokens of 8 heads in
-// 18 us, 5.6 TB/s) and by launch and load latency for single tokens (64 of them
+// 18 us in a graph, 5.6 TB/s, 20 one by one) and by launch and load latency for single tokens (64 of them
 // in 4.4 us).  Finding the runs by one comparison per thread instead of a loop
 // over the window, and the quotients by products, were 100 -> 26 us of the 16K
 // tokens; magnitudes compared as integers 26 -> 18.

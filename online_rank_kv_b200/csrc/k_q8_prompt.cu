@@ -41,10 +41,12 @@
 // over, their values' product, the scores after next, softmax -- do not overlap
 // fully.  Whatever lengthens the way from scores to weights shows at once: the
 // sums taken behind the hand-over instead of before it were 683 -> 574 us of an
-// 8192-token prompt (32 query, 8 KV heads).  That prompt takes 553 us: 994
-// TFLOP/s, 60 % of the measured matrix rate; 596 us in long runs, at the power
-// limit.  Tried and slower: 128-column scores in one buffer (726 against 659),
-// no maximum but a check of the sums (645 against 558).
+// 8192-token prompt (32 query, 8 KV heads).  That prompt takes 557 us in a graph of
+// four, 987 TFLOP/s, 60 % of the measured matrix rate, and 610 us in long runs, 55 %,
+// at the power limit.  A cap takes the prompt to 1115 us, a distance bias to 1010:
+// more arithmetic on the softmax warps, whose chain is the bound.  Tried and
+// slower: 128-column scores in one buffer (726 against 659), no maximum but a check
+// of the sums (645 against 558).
 #include "q8_common.cuh"
 #include "tc_util.cuh"
 

@@ -39,8 +39,9 @@
 // kernel.
 //
 // What bounds it: DRAM for long caches (8 KV heads, 32 query heads, int8: 8 x 32K
-// tokens 97 us, 5.5 TB/s, 84 % of the measured copy rate; 96 ragged requests of up
-// to 16K tokens, e4m3, capped, 294 us, 5.9 TB/s), for short ones the latency of
+// tokens 98 us on one GPU and 104 on another, 84 and 79 % of the measured copy rate;
+// 96 ragged requests of up to 16K tokens, e4m3, capped, 304 and 323 us, 88 and 83 %;
+// fp32 queries, with twice the products, 8 x 32K tokens 126 us, 65 %), for short ones the latency of
 // about six dependent memory accesses, two launches and the first fetch of the
 // code (1 request of 1K tokens 12 us, of 64 tokens 9 us with one launch).
 #include <cuda.h>
