@@ -39,8 +39,8 @@
 // kernel.
 //
 // What bounds it: DRAM for long caches (8 KV heads, 32 query heads, int8: 8 x 32K
-// tokens 98 us on one GPU and 104 on another, 84 and 79 % of the measured copy rate;
-// 96 ragged requests of up to 16K tokens, e4m3, capped, 304 and 323 us, 88 and 83 %;
+// tokens 98 us on one GPU and 105 on another, 84 and 78 % of the measured copy rate;
+// 96 ragged requests of up to 16K tokens, e4m3, capped, 304 and 326 us, 88 and 82 %;
 // fp32 queries, with twice the products, 8 x 32K tokens 126 us, 65 %), for short ones the latency of
 // about six dependent memory accesses, two launches and the first fetch of the
 // code (1 request of 1K tokens 12 us, of 64 tokens 9 us with one launch).
@@ -515,8 +515,8 @@ __global__ void __launch_bounds__(Shape<NT, F32>::kThreads, 1) q8_rows_kernel(co
                 __syncwarp();
             }
             const int64_t block = (int64_t)max(this_page, 0) * p.kv_heads + at.h;
-            const float sk = p.k_scale[block];
-            const float sv = p.v_scale[block];
+            // (a page that is not there has no scales: those of page 0 may be anything)
+            const float sk = this_page < 0 ? 0.f : p.k_scale[block], sv = this_page < 0 ? 0.f : p.v_scale[block];
             const uint32_t kb = ring_at + stage * kStageBytes, vb = kb + kStoreBytes;
             stage = stage + 1 == kStages ? 0 : stage + 1;
 

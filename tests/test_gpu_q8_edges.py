@@ -464,3 +464,22 @@ def test_calls_on_given_streams_inside_a_capture(new):
         assert torch.equal(eager.out[:m], captured.out[:m])
         assert torch.equal(eager.pages.k.view(torch.uint8), captured.pages.k.view(torch.uint8))
     assert captured.pages.status() == 0 and captured.plan.status.item() == 0
+
+
+@pytest.mark.parametrize("scale", [1e-40, 1e-45, float("nan"), float("inf"), -1.0])
+@pytest.mark.parametrize("dtype,new", [("bf16", 1), ("f32", 3), ("bf16", 130)])
+def test_hidden_pages_read_no_scale(scale, dtype, new):
+    """A table entry outside the pool hides its tokens, whatever stands in the
+    scales of pages that nobody holds (page 0 among them)."""
+    c = Case([640, 300], [new, new], 2, 4, ref.INT8, dtype, seed=47)
+    spare = next(p for p in range(c.kc.shape[0]) if p and p not in c.table)
+    for x in (c.kc, c.ks, c.vc, c.vs):
+        x[spare] = x[0]
+    c.table[c.table == 0] = spare
+    want = Case([640, 300], [new, new], 2, 4, ref.INT8, dtype, seed=47).run()
+    c.ks[0], c.vs[0] = scale, scale
+    assert torch.equal(c.run(), want)
+    c.table[0, 3], c.table[1, 1] = -1, 10 ** 6
+    got = c.run()
+    c.ks[0], c.vs[0], c.store_t = 1.0, 1.0, None
+    assert torch.isfinite(got).all() and torch.equal(got, c.run())
